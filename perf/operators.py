@@ -274,7 +274,7 @@ def _plain_plan(s):
     shrink = sound & (delta < 0)
     give = torch.where(shrink, have - want, 0)
     taken, given = torch.where(granted, need, 0).sum(), give.sum()
-    whole = (head >= 0) & (head < n) & (count >= 0) & (count <= n) & (count - taken + given <= n)
+    whole = (head >= 0) & (head < n) & (count >= 0) & (count <= n) & (count + given <= n)
     granted, shrink = granted & whole, shrink & whole
     # Pages out of the ring, and back behind its end.
     j = torch.arange(c["max_pages"], device=DEV)
