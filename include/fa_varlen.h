@@ -355,6 +355,143 @@ fa_status fa_varlen_bwd_schedule_ex(const int64_t *seq_lens_q, const int64_t *se
                                     int64_t tail_items, int32_t head_pairs, int32_t *items,
                                     int64_t capacity, int64_t *n_items);
 
+/* ---------------------------------------------------------------------------
+ * Paged key/value cache: the attention above for one new token per sequence
+ * (additions of this library; the FAG-V2 page has no counterpart).
+ *
+ *   fa_paged_plan    block tables and slot maps from the requests' lengths
+ *   fa_paged_write   new key / value rows into the cache, at those slots
+ *   fa_paged_decode  y, and the softmax statistics, of one query row per
+ *                    request over its cached keys
+ *
+ * Cache.  k_pages and v_pages hold num_pages pages of page_size tokens;
+ * element (page, token, head, d) of either sits at
+ *     page*page_stride + token*token_stride + head*head_stride + d
+ * (strides in elements, the same for both), so token-major pages, head-major
+ * pages and pages that hold K beside V are all covered.  Both bases and the
+ * three strides must be multiples of 16 bytes, and the strides at least
+ * head_dim (FA_ERR_INVALID otherwise; the stride of an axis with one entry
+ * is not looked at).  Pages must not overlap.
+ *
+ * Table.  block_table is [batch, table_stride] int32 on the device, of which
+ * a row's first max_pages entries count: key j of request b is token
+ * j % page_size of page block_table[b, j / page_size].  Entries behind a
+ * request's last page are never read.  Requests may share pages that
+ * nobody writes.  seq_lens: int32 [batch] on the device, the keys that each
+ * request holds.
+ *
+ * Everything that a call reads beyond its scalars is on the device, so the
+ * calls of a decoding step can be captured once into a CUDA graph and
+ * replayed; nothing synchronises.  What the host cannot check, the kernels
+ * do: they add bits to *error (device int32, or NULL), which they never
+ * clear, and read or write no memory through a bad value:
+ *   FA_PAGED_EXHAUSTED   plan: the free pages did not suffice for a request
+ *   FA_PAGED_ROW_FULL    plan: a request would pass max_pages pages
+ *   FA_PAGED_ROWS        plan: a request's new rows pass max_tokens
+ *   FA_PAGED_BAD_PAGE    a page id outside [0, num_pages) in a place that
+ *                        counts (plan: its slots become -1; decode: its keys
+ *                        take no part)
+ *   FA_PAGED_BAD_LENGTH  a length below 0 or above max_pages * page_size
+ *                        (plan: the request is left alone; decode: the
+ *                        length is clamped)
+ *   FA_PAGED_BAD_POOL    plan: head or count outside the ring, or more pages
+ *                        given back than it has room for; the call changes
+ *                        nothing
+ *   FA_PAGED_BAD_SLOT    write: a slot at or above num_pages * page_size,
+ *                        whose row is skipped
+ * Limits (FA_ERR_INVALID): batch in [1, 2048]; num_pages in [1, 2^31);
+ * page_size in [1, 65536]; max_pages >= 1 with max_pages * page_size <= 2^30;
+ * table_stride >= max_pages.  Head counts and dims as above.
+ * ------------------------------------------------------------------------- */
+enum {
+  FA_PAGED_EXHAUSTED = 1,
+  FA_PAGED_ROW_FULL = 2,
+  FA_PAGED_ROWS = 4,
+  FA_PAGED_BAD_PAGE = 8,
+  FA_PAGED_BAD_LENGTH = 16,
+  FA_PAGED_BAD_POOL = 32,
+  FA_PAGED_BAD_SLOT = 64
+};
+
+/* Grows and shrinks the requests by delta[b] tokens each (device int32
+ * [batch]) and maps the new tokens to cache slots.
+ *   delta > 0   the request takes that many tokens, and the pages that they
+ *               need beyond those it holds; 0: it stays as it is
+ *   delta < 0   its length falls to max(0, length + delta) (any value at or
+ *               below -length ends it) and the pages behind the new length
+ *               go back to the pool
+ * Pool.  free_pages is a ring of num_pages int32 page ids; free_state is
+ * int64 {head, count}: the free pages are free_pages[(head + i) % num_pages],
+ * i < count.  A fresh pool is free_pages[i] = i, {0, num_pages}.  Pages are
+ * taken in request order from the head and given back in request order
+ * behind the end; those given back by a call serve the next one.
+ * A request is refused as a whole (length and pages unchanged, slots -1, an
+ * error bit) where it would pass max_pages pages, its rows would pass
+ * max_tokens, or the pages taken up to and including it exceed count; a
+ * request that needs no page is not refused for the pool's sake.
+ * Rows.  The new tokens are packed as in TND: request b owns rows
+ * [cu_tokens[b], cu_tokens[b] + max(delta[b], 0)), refused or not.
+ *   slots         int64 [max_tokens]: page * page_size + token of each row; -1
+ *                 for refused rows and for those behind the last one
+ *   cu_tokens     int64 [batch + 1]
+ *   seq_lens_out, free_state_out: lengths and pool after the call.  Either
+ *                 may be its input (updated in place).  With neither in
+ *                 place, repeating the call repeats its results.
+ * block_table and free_pages are updated in place: entries of pages taken
+ * and of pages given back are written, all others are left as they were (so
+ * are the table's entries of pages given back).  No two calls on one pool may
+ * overlap.  max_tokens in [0, 2^31); slots may be NULL when it is 0. */
+fa_status fa_paged_plan(int32_t *block_table, int64_t max_pages, int64_t table_stride,
+                        const int32_t *seq_lens, const int32_t *delta, int64_t batch,
+                        int32_t *free_pages, const int64_t *free_state, int64_t num_pages,
+                        int64_t page_size, int64_t *slots, int64_t max_tokens,
+                        int64_t *cu_tokens, int32_t *seq_lens_out, int64_t *free_state_out,
+                        int32_t *error, fa_stream_t stream);
+
+/* Copies row t of k and v ([tokens, head_num_kv, head_dim], rows k_stride /
+ * v_stride elements apart, heads contiguous) to cache slot slots[t] =
+ * page * page_size + token, for every t whose slot is not negative.  The rest
+ * of the cache is left as it was.  Slots must be distinct: what a slot named
+ * twice then holds is unspecified.  k and v need no alignment beyond their
+ * type's; with 16-byte aligned rows the copies are wider.  tokens in
+ * [0, 2^31); tokens == 0 returns FA_OK without a launch. */
+fa_status fa_paged_write(const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                         const int64_t *slots, int64_t tokens, void *k_pages, void *v_pages,
+                         int64_t num_pages, int64_t page_size, int64_t head_num_kv,
+                         int64_t head_dim, int64_t page_stride, int64_t token_stride,
+                         int64_t head_stride, fa_dtype dtype, int32_t *error,
+                         fa_stream_t stream);
+
+/* Workspace of fa_paged_decode in bytes, on the current device.  It does not
+ * depend on the lengths.  A workspace serves one call at a time: calls that
+ * may overlap (other streams, graphs replayed at once) need one each. */
+fa_status fa_paged_decode_workspace_size(int64_t batch, int64_t head_num, int64_t head_num_kv,
+                                         int64_t head_dim, fa_dtype dtype,
+                                         size_t *workspace_bytes);
+
+/* Attention of one query row per request: row b of q ([batch, head_num,
+ * head_dim], rows q_stride elements apart, heads contiguous) stands at
+ * position seq_lens[b] - 1 and sees the keys j < seq_lens[b] with
+ * j >= seq_lens[b] - 1 - pre_tokens (its own among them: write the step's rows
+ * first).  Formulas, grouped heads, types and head dims are those of
+ * fa_varlen_fwd; pre_tokens likewise.
+ *   y             [batch, head_num, head_dim], rows y_stride elements apart
+ *   softmax_max, softmax_sum: float32 [batch, head_num, 8], all lanes
+ *                 written, as fa_varlen_fwd writes them; or both NULL
+ * A request with no key to see (length 0, or pre_tokens < 0), or whose every
+ * score is -inf, gets y = 0, max = -inf, sum = 0.  What the cache holds behind
+ * a request's length, infinities and NaN too, has no influence.  The result
+ * does not change from run to run on one device (fixed add order). */
+fa_status fa_paged_decode(const void *q, int64_t q_stride, const void *k_pages,
+                          const void *v_pages, int64_t num_pages, int64_t page_size,
+                          int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                          const int32_t *block_table, int64_t max_pages, int64_t table_stride,
+                          const int32_t *seq_lens, int64_t batch, int64_t head_num,
+                          int64_t head_num_kv, int64_t head_dim, fa_dtype dtype, double scale,
+                          int64_t pre_tokens, void *y, int64_t y_stride, float *softmax_max,
+                          float *softmax_sum, int32_t *error, void *workspace,
+                          size_t workspace_bytes, fa_stream_t stream);
+
 /* Library version: major * 10000 + minor * 100 + patch. */
 int32_t fa_varlen_version(void);
 

@@ -15,7 +15,9 @@ restates.
 Parity status: every public function here is pinned by the CPU tests in
 ``tests/test_oracle.py`` (finite differences, closed forms, invariants, torch
 fp64 autograd and the page's own call example).  No function is "parity
-unpinned".
+unpinned".  The paged-cache functions, which no page defines, are pinned by
+``tests/test_paged_oracle.py`` (against ``varlen_forward``, hand-worked plans
+and the conservation of pages).
 """
 
 from .attention import (  # noqa: F401
@@ -32,3 +34,4 @@ from .attention import (  # noqa: F401
     mask_bit_offsets,
     cu_seqlens,
 )
+from .paged import paged_plan, paged_write, paged_decode  # noqa: F401

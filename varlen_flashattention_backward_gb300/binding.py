@@ -19,6 +19,10 @@ FA_OK, FA_ERR_NULLPTR, FA_ERR_INVALID, FA_ERR_UNSUPPORTED = 0, 1, 2, 3
 FA_ERR_WORKSPACE, FA_ERR_CUDA, FA_ERR_TIMEOUT = 4, 5, 6
 FA_BWD_AUTO, FA_BWD_SIMT, FA_BWD_TCGEN05 = 0, 1, 2
 
+# Bits of the paged entry points' error word.
+FA_PAGED_EXHAUSTED, FA_PAGED_ROW_FULL, FA_PAGED_ROWS, FA_PAGED_BAD_PAGE = 1, 2, 4, 8
+FA_PAGED_BAD_LENGTH, FA_PAGED_BAD_POOL, FA_PAGED_BAD_SLOT = 16, 32, 64
+
 _DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 _LIB = None
@@ -83,6 +87,13 @@ _SIGS = {
     "fa_varlen_bwd_schedule_ex": ([_pi64, _pi64, _i64, _i64, _i64, _i64, _i32, _i64, _i64, _i32,
                                    _i64, _i64, _i32, ctypes.POINTER(ctypes.c_int32), _i64, _pi64],
                                   _i32),
+    "fa_paged_plan": ([_vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp,
+                       _vp, _vp, _vp], _i32),
+    "fa_paged_write": ([_vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp] + [_i64] * 7 +
+                       [_i32, _vp, _vp], _i32),
+    "fa_paged_decode_workspace_size": ([_i64, _i64, _i64, _i64, _i32, _psz], _i32),
+    "fa_paged_decode": ([_vp, _i64, _vp, _vp] + [_i64] * 5 + [_vp, _i64, _i64, _vp] + [_i64] * 4 +
+                        [_i32, _f64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
 }
 
 EXPORTS = tuple(_SIGS)
@@ -369,3 +380,219 @@ def gen_keep_mask(nbits: int, seed: int, keep_prob: float, device="cuda", out=No
     _check(lib().fa_gen_keep_mask(_ptr(out), int(nbits), int(seed) & (2 ** 64 - 1),
                                   float(keep_prob), _stream(stream)), "fa_gen_keep_mask")
     return out
+
+
+# ---------------------------------------------------------------------------
+# Paged key/value cache
+# ---------------------------------------------------------------------------
+
+def _want(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+class _OnDevice:
+    """Makes `tensor`'s device and `stream` (default: the device's current
+    stream) the ones that a call allocates and launches on, and back."""
+
+    __slots__ = ("raw", "_back", "_ctx")
+
+    def __init__(self, tensor, stream):
+        index = tensor.device.index
+        self._back = self._ctx = None
+        if stream is not None:
+            _want(stream.device.index == index, "stream of another device")
+            self._ctx = torch.cuda.stream(stream)
+            self._ctx.__enter__()
+            self.raw = stream.cuda_stream
+            return
+        now = torch.cuda.current_device()
+        if now != index:
+            self._back = now
+            torch.cuda.set_device(index)
+        self.raw = torch.cuda.current_stream().cuda_stream
+
+    def close(self):
+        if self._ctx is not None:
+            self._ctx.__exit__(None, None, None)
+        if self._back is not None:
+            torch.cuda.set_device(self._back)
+
+
+def _on(device, **tensors):
+    """Each given tensor is on `device`, a CUDA device."""
+    _want(device.type == "cuda", f"expected tensors on a CUDA device, got {device}")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _plain(t, dtype, shape, name):
+    """A contiguous tensor of this type and shape."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} {shape}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+
+
+def _table(t, name="block_table"):
+    """(max_pages, stride) of an int32 [batch, max_pages] table."""
+    _want(t.dim() == 2 and t.dtype == torch.int32 and (t.shape[1] <= 1 or t.stride(1) == 1),
+          f"{name}: expected int32 [batch, max_pages] with adjacent entries")
+    return t.shape[1], (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def _pages(k_pages, v_pages):
+    """Shape and strides of the cache: both [pages, page_size, heads, dim]."""
+    shape, strides = k_pages.shape, k_pages.stride()
+    _want(len(shape) == 4 and v_pages.shape == shape and v_pages.dtype == k_pages.dtype and
+          k_pages.dtype in _DTYPE, "k_pages and v_pages: two [pages, page_size, heads, dim] tensors "
+          "of one type (fp32, fp16 or bf16)")
+    other = v_pages.stride()
+    _want(other == strides or all(a == b or n == 1 for a, b, n in zip(other, strides, shape)),
+          "k_pages and v_pages: different strides")
+    _want(strides[3] == 1, "k_pages and v_pages: adjacent dims")
+    return shape, strides
+
+
+def _rows(t, shape, dtype, name):
+    """Row stride of a [rows, heads, dim] tensor whose heads are contiguous."""
+    _want(tuple(t.shape) == shape and t.dtype == dtype, f"{name}: expected {dtype} {shape}, got "
+          f"{t.dtype} {tuple(t.shape)}")
+    stride = t.stride()
+    _want(stride[2] == 1 and (shape[1] == 1 or stride[1] == shape[2]),
+          f"{name}: heads and dims of a row must be contiguous")
+    return stride[0]
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def paged_plan(block_table, seq_lens, delta, free_pages, free_state, page_size, max_tokens,
+               slots=None, cu_tokens=None, seq_lens_out=None, free_state_out=None, error=None,
+               stream=None):
+    """(slots, cu_tokens, seq_lens_out, free_state_out) of fa_paged_plan:
+    requests grow or shrink by ``delta`` tokens, ``block_table`` and the ring
+    ``free_pages`` are updated in place, and each new token gets its slot.
+    Pass ``seq_lens_out=seq_lens, free_state_out=free_state`` to update those
+    in place too.  ``error``: int32 [1], to which error bits are added."""
+    dev = block_table.device
+    _on(dev, seq_lens=seq_lens, delta=delta, free_pages=free_pages, free_state=free_state,
+        slots=slots, cu_tokens=cu_tokens, seq_lens_out=seq_lens_out,
+        free_state_out=free_state_out, error=error)
+    max_pages, stride = _table(block_table)
+    b, max_tokens = block_table.shape[0], int(max_tokens)
+    _plain(seq_lens, torch.int32, (b,), "seq_lens")
+    _plain(delta, torch.int32, (b,), "delta")
+    _plain(free_state, torch.int64, (2,), "free_state")
+    _want(free_pages.dim() == 1 and free_pages.dtype == torch.int32 and
+          free_pages.is_contiguous(), "free_pages: expected contiguous int32 [num_pages]")
+    if error is not None:
+        _plain(error, torch.int32, (1,), "error")
+    on = _OnDevice(block_table, stream)
+    try:
+        if slots is None:
+            slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+        else:
+            _plain(slots, torch.int64, (max_tokens,), "slots")
+        if cu_tokens is None:
+            cu_tokens = torch.empty(b + 1, dtype=torch.int64, device=dev)
+        else:
+            _plain(cu_tokens, torch.int64, (b + 1,), "cu_tokens")
+        if seq_lens_out is None:
+            seq_lens_out = torch.empty(b, dtype=torch.int32, device=dev)
+        else:
+            _plain(seq_lens_out, torch.int32, (b,), "seq_lens_out")
+        if free_state_out is None:
+            free_state_out = torch.empty(2, dtype=torch.int64, device=dev)
+        else:
+            _plain(free_state_out, torch.int64, (2,), "free_state_out")
+        _check(lib().fa_paged_plan(
+            block_table.data_ptr(), max_pages, stride, seq_lens.data_ptr(), delta.data_ptr(), b,
+            free_pages.data_ptr(), free_state.data_ptr(), free_pages.numel(), int(page_size),
+            slots.data_ptr(), max_tokens, cu_tokens.data_ptr(), seq_lens_out.data_ptr(),
+            free_state_out.data_ptr(), _addr(error), on.raw), "fa_paged_plan")
+    finally:
+        on.close()
+    return slots, cu_tokens, seq_lens_out, free_state_out
+
+
+def paged_write(k, v, slots, k_pages, v_pages, error=None, stream=None):
+    """Rows of ``k`` and ``v`` ([tokens, heads, dim]) into the cache at
+    ``slots`` (fa_paged_write); negative slots are skipped.  The cache is
+    [pages, page_size, heads, dim]; head-major pages are a transposed view."""
+    shape, strides = _pages(k_pages, v_pages)
+    _on(k_pages.device, v_pages=v_pages, k=k, v=v, slots=slots, error=error)
+    tokens = slots.numel()
+    ks = _rows(k, (tokens, shape[2], shape[3]), k_pages.dtype, "k")
+    vs = _rows(v, (tokens, shape[2], shape[3]), k_pages.dtype, "v")
+    _plain(slots, torch.int64, (tokens,), "slots")
+    if error is not None:
+        _plain(error, torch.int32, (1,), "error")
+    on = _OnDevice(k_pages, stream)
+    try:
+        _check(lib().fa_paged_write(
+            k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), tokens, k_pages.data_ptr(),
+            v_pages.data_ptr(), shape[0], shape[1], shape[2], shape[3], strides[0], strides[1],
+            strides[2], _DTYPE[k_pages.dtype], _addr(error), on.raw), "fa_paged_write")
+    finally:
+        on.close()
+
+
+def paged_decode_workspace_size(batch, n, n_kv, d, dtype) -> int:
+    """Bytes of the workspace of ``paged_decode`` on the current device."""
+    out = ctypes.c_size_t(0)
+    _check(lib().fa_paged_decode_workspace_size(int(batch), int(n), int(n_kv), int(d),
+                                                _DTYPE[dtype], ctypes.byref(out)),
+           "fa_paged_decode_workspace_size")
+    return out.value
+
+
+def paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, pre_tokens=2 ** 31 - 1,
+                 y=None, stats=False, softmax_max=None, softmax_sum=None, workspace=None,
+                 error=None, stream=None):
+    """(y, softmax_max, softmax_sum) of one query row per request over its
+    cached keys (fa_paged_decode).  The statistics ([batch, heads, 8], as
+    ``fwd`` gives them) are computed with ``stats`` or when their tensors
+    are given, and None otherwise."""
+    shape, strides = _pages(k_pages, v_pages)
+    dev = k_pages.device
+    _on(dev, v_pages=v_pages, q=q, block_table=block_table, seq_lens=seq_lens, y=y,
+        softmax_max=softmax_max, softmax_sum=softmax_sum, workspace=workspace, error=error)
+    max_pages, table_stride = _table(block_table)
+    b = block_table.shape[0]
+    _want(q.dim() == 3, "q: expected [batch, heads, dim]")
+    n, d = q.shape[1], shape[3]
+    qs = _rows(q, (b, n, d), k_pages.dtype, "q")
+    _plain(seq_lens, torch.int32, (b,), "seq_lens")
+    if error is not None:
+        _plain(error, torch.int32, (1,), "error")
+    on = _OnDevice(k_pages, stream)
+    try:
+        if y is None:
+            y = torch.empty((b, n, d), dtype=q.dtype, device=dev)
+            ys = n * d
+        else:
+            ys = _rows(y, (b, n, d), k_pages.dtype, "y")
+        if stats or softmax_max is not None or softmax_sum is not None:
+            if softmax_max is None:
+                softmax_max = torch.empty((b, n, 8), dtype=torch.float32, device=dev)
+            if softmax_sum is None:
+                softmax_sum = torch.empty((b, n, 8), dtype=torch.float32, device=dev)
+            _plain(softmax_max, torch.float32, (b, n, 8), "softmax_max")
+            _plain(softmax_sum, torch.float32, (b, n, 8), "softmax_sum")
+        if workspace is None:
+            workspace = torch.empty(paged_decode_workspace_size(b, n, shape[2], d, q.dtype),
+                                    dtype=torch.uint8, device=dev)
+        else:
+            _want(workspace.is_contiguous(), "workspace: expected contiguous")
+        _check(lib().fa_paged_decode(
+            q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), shape[0], shape[1],
+            strides[0], strides[1], strides[2], block_table.data_ptr(), max_pages, table_stride,
+            seq_lens.data_ptr(), b, n, shape[2], d, _DTYPE[q.dtype], float(scale),
+            int(pre_tokens), y.data_ptr(), ys, _addr(softmax_max), _addr(softmax_sum),
+            _addr(error), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            on.raw), "fa_paged_decode")
+    finally:
+        on.close()
+    return y, softmax_max, softmax_sum

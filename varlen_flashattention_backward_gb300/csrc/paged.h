@@ -1,0 +1,67 @@
+// Declarations shared by the paged-cache entry points (paged_abi.cpp) and
+// their kernels (paged_plan.cu, paged_write.cu, paged_decode.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fa_varlen.h"
+
+namespace fav {
+
+struct PlanParams {
+  int32_t *table;
+  int64_t table_stride;
+  const int32_t *lens, *delta;
+  int32_t *ring;
+  const int64_t *state;
+  int64_t *slots, *cu;
+  int32_t *lens_out;
+  int64_t *state_out;
+  int32_t *error;
+  int64_t max_tokens;
+  int batch, max_pages, num_pages, page_size;
+};
+
+struct WriteParams {
+  const void *k, *v;
+  int64_t k_stride, v_stride;
+  const int64_t *slots;
+  void *kc, *vc;
+  int64_t n_slots;
+  int64_t page_stride, token_stride, head_stride;
+  int32_t *error;
+  int tokens, page_size, n_kv, d;
+};
+
+struct DecodeParams {
+  const void *q;
+  int64_t q_stride;
+  const void *kc, *vc;
+  int64_t page_stride, token_stride, head_stride;
+  const int32_t *table;
+  int64_t table_stride;
+  const int32_t *lens;
+  void *y;
+  int64_t y_stride;
+  float *smax, *ssum;
+  int32_t *error;
+  float *part;        // partial results: two slots per CTA (see paged_decode.cu)
+  int32_t *meta;      // four words per CTA
+  int num_pages, page_size, page_shift;   // page_shift: log2(page_size), or -1
+  int max_pages, batch, n, n_kv, d, group;
+  int pre;            // pre_tokens clamped to [-1, 2^30]
+  int grid;           // CTAs of the main kernel
+  float scale, scale_log2;
+};
+
+// Largest workspace grid of fa_paged_decode: CTAs per SM.
+constexpr int kDecodeCtasPerSm = 2;
+// Query heads of one key head that a CTA takes at a time.
+int decode_rows(fa_dtype dt, int group);
+
+cudaError_t launch_paged_plan(const PlanParams &p, cudaStream_t s);
+cudaError_t launch_paged_write(const WriteParams &p, fa_dtype dt, cudaStream_t s);
+cudaError_t launch_paged_decode(const DecodeParams &p, fa_dtype dt, int sms, cudaStream_t s);
+
+}  // namespace fav
