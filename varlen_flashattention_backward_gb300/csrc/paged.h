@@ -59,6 +59,8 @@ struct DecodeParams {
 constexpr int kDecodeCtasPerSm = 2;
 // Query heads of one key head that a CTA takes at a time.
 int decode_rows(fa_dtype dt, int group);
+// Floats of one partial result in the workspace.
+size_t decode_part_floats(int rows, int d);
 
 cudaError_t launch_paged_plan(const PlanParams &p, cudaStream_t s);
 cudaError_t launch_paged_write(const WriteParams &p, fa_dtype dt, cudaStream_t s);

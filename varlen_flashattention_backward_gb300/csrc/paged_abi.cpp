@@ -98,7 +98,8 @@ DecodeLayout decode_layout(int ctas, int rows, int64_t head_dim) {
   DecodeLayout L;
   L.meta = 0;
   L.part = align_up(size_t(ctas) * 4 * sizeof(int32_t));
-  L.total = L.part + align_up(size_t(ctas) * 2 * rows * size_t(head_dim + 2) * sizeof(float));
+  L.total = L.part + align_up(size_t(ctas) * 2 * decode_part_floats(rows, int(head_dim)) *
+                               sizeof(float));
   return L;
 }
 
