@@ -9,6 +9,7 @@ not been built, the first call raises: there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -386,86 +387,92 @@ def gen_keep_mask(nbits: int, seed: int, keep_prob: float, device="cuda", out=No
 # Paged key/value cache
 # ---------------------------------------------------------------------------
 
-def _want(ok, what):
-    if not ok:
-        raise ValueError(what)
+# A decoding step makes these calls for every layer, so what they check is
+# arranged to cost little: one expression of integer comparisons per tensor,
+# and the sentence that explains a refusal is only put together for one.
 
+class _On:
+    """Makes `stream` (or, without one, the current stream of device `index`)
+    the one that a call allocates on, and gives its handle."""
 
-class _OnDevice:
-    """Makes `tensor`'s device and `stream` (default: the device's current
-    stream) the ones that a call allocates and launches on, and back."""
+    __slots__ = ("_ctx",)
 
-    __slots__ = ("raw", "_back", "_ctx")
-
-    def __init__(self, tensor, stream):
-        index = tensor.device.index
-        self._back = self._ctx = None
-        if stream is not None:
-            _want(stream.device.index == index, "stream of another device")
+    def __init__(self, index, stream):
+        if stream is None:
+            self._ctx = torch.cuda.device(index)
+        elif stream.device.index != index:
+            raise ValueError("stream of another device")
+        else:
             self._ctx = torch.cuda.stream(stream)
-            self._ctx.__enter__()
-            self.raw = stream.cuda_stream
-            return
-        now = torch.cuda.current_device()
-        if now != index:
-            self._back = now
-            torch.cuda.set_device(index)
-        self.raw = torch.cuda.current_stream().cuda_stream
 
-    def close(self):
-        if self._ctx is not None:
-            self._ctx.__exit__(None, None, None)
-        if self._back is not None:
-            torch.cuda.set_device(self._back)
+    def __enter__(self):
+        self._ctx.__enter__()
+
+    def __exit__(self, *exc):
+        self._ctx.__exit__(*exc)
 
 
-def _on(device, **tensors):
-    """Each given tensor is on `device`, a CUDA device."""
-    _want(device.type == "cuda", f"expected tensors on a CUDA device, got {device}")
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+def _elsewhere(index, stream):
+    """Whether a call on device `index` has to switch device or stream."""
+    return stream is not None or torch._C._cuda_getDevice() != index
 
 
-def _plain(t, dtype, shape, name):
-    """A contiguous tensor of this type and shape."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {dtype} {shape}, got {t.dtype} "
-                         f"{tuple(t.shape)}")
+def _raw_stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _table(t, name="block_table"):
+def _refuse(name, t, expected, index=None):
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    raise ValueError(f"{name}: expected {expected}, got {t.dtype} {tuple(t.shape)} with strides "
+                     f"{t.stride()}")
+
+
+def _device_of(t, name):
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name}: expected a tensor on a CUDA device, got {t.device}")
+    return index
+
+
+def _flat(t, dtype, count, index, name):
+    """A contiguous one-dimensional tensor of `count` entries."""
+    if not (t.get_device() == index and t.dtype is dtype and t.dim() == 1 and
+            t.numel() == count and t.is_contiguous()):
+        _refuse(name, t, f"contiguous {dtype} [{count}]", index)
+    return t.data_ptr()
+
+
+def _table(t, index):
     """(max_pages, stride) of an int32 [batch, max_pages] table."""
-    _want(t.dim() == 2 and t.dtype == torch.int32 and (t.shape[1] <= 1 or t.stride(1) == 1),
-          f"{name}: expected int32 [batch, max_pages] with adjacent entries")
-    return t.shape[1], (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    shape, stride = t.shape, t.stride()
+    if not (len(shape) == 2 and t.dtype is torch.int32 and t.get_device() == index and
+            (stride[1] == 1 or shape[1] <= 1)):
+        _refuse("block_table", t, "int32 [batch, max_pages] with adjacent entries", index)
+    return shape[1], (stride[0] if shape[0] > 1 else shape[1])
 
 
-def _pages(k_pages, v_pages):
+def _pages(k_pages, v_pages, index):
     """Shape and strides of the cache: both [pages, page_size, heads, dim]."""
-    shape, strides = k_pages.shape, k_pages.stride()
-    _want(len(shape) == 4 and v_pages.shape == shape and v_pages.dtype == k_pages.dtype and
-          k_pages.dtype in _DTYPE, "k_pages and v_pages: two [pages, page_size, heads, dim] tensors "
-          "of one type (fp32, fp16 or bf16)")
-    other = v_pages.stride()
-    _want(other == strides or all(a == b or n == 1 for a, b, n in zip(other, strides, shape)),
-          "k_pages and v_pages: different strides")
-    _want(strides[3] == 1, "k_pages and v_pages: adjacent dims")
-    return shape, strides
+    shape, stride, dtype = k_pages.shape, k_pages.stride(), k_pages.dtype
+    if not (len(shape) == 4 and stride[3] == 1 and dtype in _DTYPE):
+        _refuse("k_pages and v_pages", k_pages, "fp32, fp16 or bf16 [pages, page_size, heads, dim] "
+                "with adjacent dims")
+    if not (v_pages.shape == shape and v_pages.dtype is dtype and v_pages.get_device() == index and
+            (v_pages.stride() == stride or
+             all(x == y or n == 1 for x, y, n in zip(v_pages.stride(), stride, shape)))):
+        _refuse("k_pages and v_pages", v_pages, f"both {dtype} {tuple(shape)} with strides {stride}",
+                index)
+    return shape, stride
 
 
-def _rows(t, shape, dtype, name):
+def _rows(t, rows, heads, dim, dtype, index, name):
     """Row stride of a [rows, heads, dim] tensor whose heads are contiguous."""
-    _want(tuple(t.shape) == shape and t.dtype == dtype, f"{name}: expected {dtype} {shape}, got "
-          f"{t.dtype} {tuple(t.shape)}")
     stride = t.stride()
-    _want(stride[2] == 1 and (shape[1] == 1 or stride[1] == shape[2]),
-          f"{name}: heads and dims of a row must be contiguous")
+    if not (t.shape == (rows, heads, dim) and t.dtype is dtype and t.get_device() == index and
+            stride[2] == 1 and (stride[1] == dim or heads == 1)):
+        _refuse(name, t, f"{dtype} {(rows, heads, dim)} with contiguous heads", index)
     return stride[0]
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
 
 
 def paged_plan(block_table, seq_lens, delta, free_pages, free_state, page_size, max_tokens,
@@ -476,44 +483,34 @@ def paged_plan(block_table, seq_lens, delta, free_pages, free_state, page_size, 
     ``free_pages`` are updated in place, and each new token gets its slot.
     Pass ``seq_lens_out=seq_lens, free_state_out=free_state`` to update those
     in place too.  ``error``: int32 [1], to which error bits are added."""
+    index = _device_of(block_table, "block_table")
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return paged_plan(block_table, seq_lens, delta, free_pages, free_state, page_size,
+                              max_tokens, slots, cu_tokens, seq_lens_out, free_state_out, error)
+    max_pages, stride = _table(block_table, index)
+    b, pages, max_tokens = block_table.shape[0], free_pages.numel(), int(max_tokens)
     dev = block_table.device
-    _on(dev, seq_lens=seq_lens, delta=delta, free_pages=free_pages, free_state=free_state,
-        slots=slots, cu_tokens=cu_tokens, seq_lens_out=seq_lens_out,
-        free_state_out=free_state_out, error=error)
-    max_pages, stride = _table(block_table)
-    b, max_tokens = block_table.shape[0], int(max_tokens)
-    _plain(seq_lens, torch.int32, (b,), "seq_lens")
-    _plain(delta, torch.int32, (b,), "delta")
-    _plain(free_state, torch.int64, (2,), "free_state")
-    _want(free_pages.dim() == 1 and free_pages.dtype == torch.int32 and
-          free_pages.is_contiguous(), "free_pages: expected contiguous int32 [num_pages]")
-    if error is not None:
-        _plain(error, torch.int32, (1,), "error")
-    on = _OnDevice(block_table, stream)
-    try:
-        if slots is None:
-            slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
-        else:
-            _plain(slots, torch.int64, (max_tokens,), "slots")
-        if cu_tokens is None:
-            cu_tokens = torch.empty(b + 1, dtype=torch.int64, device=dev)
-        else:
-            _plain(cu_tokens, torch.int64, (b + 1,), "cu_tokens")
-        if seq_lens_out is None:
-            seq_lens_out = torch.empty(b, dtype=torch.int32, device=dev)
-        else:
-            _plain(seq_lens_out, torch.int32, (b,), "seq_lens_out")
-        if free_state_out is None:
-            free_state_out = torch.empty(2, dtype=torch.int64, device=dev)
-        else:
-            _plain(free_state_out, torch.int64, (2,), "free_state_out")
-        _check(lib().fa_paged_plan(
-            block_table.data_ptr(), max_pages, stride, seq_lens.data_ptr(), delta.data_ptr(), b,
-            free_pages.data_ptr(), free_state.data_ptr(), free_pages.numel(), int(page_size),
-            slots.data_ptr(), max_tokens, cu_tokens.data_ptr(), seq_lens_out.data_ptr(),
-            free_state_out.data_ptr(), _addr(error), on.raw), "fa_paged_plan")
-    finally:
-        on.close()
+    if slots is None:
+        slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+    if cu_tokens is None:
+        cu_tokens = torch.empty(b + 1, dtype=torch.int64, device=dev)
+    if seq_lens_out is None:
+        seq_lens_out = torch.empty(b, dtype=torch.int32, device=dev)
+    if free_state_out is None:
+        free_state_out = torch.empty(2, dtype=torch.int64, device=dev)
+    i32, i64 = torch.int32, torch.int64
+    _check(lib().fa_paged_plan(
+        block_table.data_ptr(), max_pages, stride, _flat(seq_lens, i32, b, index, "seq_lens"),
+        _flat(delta, i32, b, index, "delta"), b,
+        _flat(free_pages, i32, pages, index, "free_pages"),
+        _flat(free_state, i64, 2, index, "free_state"), pages, int(page_size),
+        _flat(slots, i64, max_tokens, index, "slots"), max_tokens,
+        _flat(cu_tokens, i64, b + 1, index, "cu_tokens"),
+        _flat(seq_lens_out, i32, b, index, "seq_lens_out"),
+        _flat(free_state_out, i64, 2, index, "free_state_out"),
+        None if error is None else _flat(error, i32, 1, index, "error"), _raw_stream(index)),
+        "fa_paged_plan")
     return slots, cu_tokens, seq_lens_out, free_state_out
 
 
@@ -521,22 +518,19 @@ def paged_write(k, v, slots, k_pages, v_pages, error=None, stream=None):
     """Rows of ``k`` and ``v`` ([tokens, heads, dim]) into the cache at
     ``slots`` (fa_paged_write); negative slots are skipped.  The cache is
     [pages, page_size, heads, dim]; head-major pages are a transposed view."""
-    shape, strides = _pages(k_pages, v_pages)
-    _on(k_pages.device, v_pages=v_pages, k=k, v=v, slots=slots, error=error)
-    tokens = slots.numel()
-    ks = _rows(k, (tokens, shape[2], shape[3]), k_pages.dtype, "k")
-    vs = _rows(v, (tokens, shape[2], shape[3]), k_pages.dtype, "v")
-    _plain(slots, torch.int64, (tokens,), "slots")
-    if error is not None:
-        _plain(error, torch.int32, (1,), "error")
-    on = _OnDevice(k_pages, stream)
-    try:
-        _check(lib().fa_paged_write(
-            k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), tokens, k_pages.data_ptr(),
-            v_pages.data_ptr(), shape[0], shape[1], shape[2], shape[3], strides[0], strides[1],
-            strides[2], _DTYPE[k_pages.dtype], _addr(error), on.raw), "fa_paged_write")
-    finally:
-        on.close()
+    index = _device_of(k_pages, "k_pages and v_pages")
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return paged_write(k, v, slots, k_pages, v_pages, error)
+    shape, strides = _pages(k_pages, v_pages, index)
+    tokens, dtype = slots.numel(), k_pages.dtype
+    _check(lib().fa_paged_write(
+        k.data_ptr(), v.data_ptr(), _rows(k, tokens, shape[2], shape[3], dtype, index, "k"),
+        _rows(v, tokens, shape[2], shape[3], dtype, index, "v"),
+        _flat(slots, torch.int64, tokens, index, "slots"), tokens, k_pages.data_ptr(),
+        v_pages.data_ptr(), *shape, strides[0], strides[1], strides[2], _DTYPE[dtype],
+        None if error is None else _flat(error, torch.int32, 1, index, "error"),
+        _raw_stream(index)), "fa_paged_write")
 
 
 def paged_decode_workspace_size(batch, n, n_kv, d, dtype) -> int:
@@ -548,6 +542,12 @@ def paged_decode_workspace_size(batch, n, n_kv, d, dtype) -> int:
     return out.value
 
 
+@functools.lru_cache(maxsize=256)
+def _decode_workspace(index, batch, n, n_kv, d, dtype):
+    """paged_decode_workspace_size of a call on device `index`, the current one."""
+    return paged_decode_workspace_size(batch, n, n_kv, d, dtype)
+
+
 def paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, pre_tokens=2 ** 31 - 1,
                  y=None, stats=False, softmax_max=None, softmax_sum=None, workspace=None,
                  error=None, stream=None):
@@ -555,44 +555,46 @@ def paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, pre_tokens=2
     cached keys (fa_paged_decode).  The statistics ([batch, heads, 8], as
     ``fwd`` gives them) are computed with ``stats`` or when their tensors
     are given, and None otherwise."""
-    shape, strides = _pages(k_pages, v_pages)
+    index = _device_of(k_pages, "k_pages and v_pages")
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, pre_tokens, y,
+                                stats, softmax_max, softmax_sum, workspace, error)
+    shape, strides = _pages(k_pages, v_pages, index)
+    max_pages, table_stride = _table(block_table, index)
+    if q.dim() != 3:
+        _refuse("q", q, "[batch, heads, dim]", index)
+    b, n, n_kv, d = block_table.shape[0], q.shape[1], shape[2], shape[3]
+    dtype = k_pages.dtype
+    qs = _rows(q, b, n, d, dtype, index, "q")
     dev = k_pages.device
-    _on(dev, v_pages=v_pages, q=q, block_table=block_table, seq_lens=seq_lens, y=y,
-        softmax_max=softmax_max, softmax_sum=softmax_sum, workspace=workspace, error=error)
-    max_pages, table_stride = _table(block_table)
-    b = block_table.shape[0]
-    _want(q.dim() == 3, "q: expected [batch, heads, dim]")
-    n, d = q.shape[1], shape[3]
-    qs = _rows(q, (b, n, d), k_pages.dtype, "q")
-    _plain(seq_lens, torch.int32, (b,), "seq_lens")
-    if error is not None:
-        _plain(error, torch.int32, (1,), "error")
-    on = _OnDevice(k_pages, stream)
-    try:
-        if y is None:
-            y = torch.empty((b, n, d), dtype=q.dtype, device=dev)
-            ys = n * d
-        else:
-            ys = _rows(y, (b, n, d), k_pages.dtype, "y")
-        if stats or softmax_max is not None or softmax_sum is not None:
-            if softmax_max is None:
-                softmax_max = torch.empty((b, n, 8), dtype=torch.float32, device=dev)
-            if softmax_sum is None:
-                softmax_sum = torch.empty((b, n, 8), dtype=torch.float32, device=dev)
-            _plain(softmax_max, torch.float32, (b, n, 8), "softmax_max")
-            _plain(softmax_sum, torch.float32, (b, n, 8), "softmax_sum")
-        if workspace is None:
-            workspace = torch.empty(paged_decode_workspace_size(b, n, shape[2], d, q.dtype),
-                                    dtype=torch.uint8, device=dev)
-        else:
-            _want(workspace.is_contiguous(), "workspace: expected contiguous")
-        _check(lib().fa_paged_decode(
-            q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), shape[0], shape[1],
-            strides[0], strides[1], strides[2], block_table.data_ptr(), max_pages, table_stride,
-            seq_lens.data_ptr(), b, n, shape[2], d, _DTYPE[q.dtype], float(scale),
-            int(pre_tokens), y.data_ptr(), ys, _addr(softmax_max), _addr(softmax_sum),
-            _addr(error), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            on.raw), "fa_paged_decode")
-    finally:
-        on.close()
+    if y is None:
+        y, ys = torch.empty((b, n, d), dtype=dtype, device=dev), n * d
+    else:
+        ys = _rows(y, b, n, d, dtype, index, "y")
+    top = total = None
+    if stats or softmax_max is not None or softmax_sum is not None:
+        if softmax_max is None:
+            softmax_max = torch.empty((b, n, 8), dtype=torch.float32, device=dev)
+        if softmax_sum is None:
+            softmax_sum = torch.empty((b, n, 8), dtype=torch.float32, device=dev)
+        for name, t in (("softmax_max", softmax_max), ("softmax_sum", softmax_sum)):
+            if not (t.shape == (b, n, 8) and t.dtype is torch.float32 and t.is_contiguous() and
+                    t.get_device() == index):
+                _refuse(name, t, f"contiguous fp32 {(b, n, 8)}", index)
+        top, total = softmax_max.data_ptr(), softmax_sum.data_ptr()
+    if workspace is None:
+        nbytes = _decode_workspace(index, b, n, n_kv, d, dtype)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+        if not (workspace.is_contiguous() and workspace.get_device() == index):
+            _refuse("workspace", workspace, "contiguous memory", index)
+    _check(lib().fa_paged_decode(
+        q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), shape[0], shape[1], strides[0],
+        strides[1], strides[2], block_table.data_ptr(), max_pages, table_stride,
+        _flat(seq_lens, torch.int32, b, index, "seq_lens"), b, n, n_kv, d, _DTYPE[dtype], scale,
+        min(max(int(pre_tokens), -1), 2 ** 40), y.data_ptr(), ys, top, total,
+        None if error is None else _flat(error, torch.int32, 1, index, "error"),
+        workspace.data_ptr(), nbytes, _raw_stream(index)), "fa_paged_decode")
     return y, softmax_max, softmax_sum

@@ -47,16 +47,19 @@ struct DecodeParams {
   float *smax, *ssum;
   int32_t *error;
   float *part;        // partial results: two slots per CTA (see paged_decode.cu)
-  int32_t *meta;      // four words per CTA
+  float *warp_part;   // ... and one per warp
   int num_pages, page_size, page_shift;   // page_shift: log2(page_size), or -1
   int max_pages, batch, n, n_kv, d, group;
+  int q_pairs, y_pairs;   // rows of q, y start on 4-byte boundaries
   int pre;            // pre_tokens clamped to [-1, 2^30]
   int grid;           // CTAs of the main kernel
+  int ranges;         // its warps
+  int unit_shift;     // log2 of the blocks in a unit of work
   float scale, scale_log2;
 };
 
-// Largest workspace grid of fa_paged_decode: CTAs per SM.
-constexpr int kDecodeCtasPerSm = 2;
+// Most warps of a CTA of the main kernel, one CTA per SM.
+constexpr int kDecodeWarps = 8;
 // Query heads of one key head that a CTA takes at a time.
 int decode_rows(fa_dtype dt, int group);
 // Floats of one partial result in the workspace.

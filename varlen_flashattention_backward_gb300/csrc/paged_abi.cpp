@@ -91,15 +91,15 @@ bool element_aligned(const void *ptr, fa_dtype dt) {
 }
 
 struct DecodeLayout {
-  size_t meta, part, total;
+  size_t part, warp_part, total;
 };
 
 DecodeLayout decode_layout(int ctas, int rows, int64_t head_dim) {
   DecodeLayout L;
-  L.meta = 0;
-  L.part = align_up(size_t(ctas) * 4 * sizeof(int32_t));
-  L.total = L.part + align_up(size_t(ctas) * 2 * decode_part_floats(rows, int(head_dim)) *
-                               sizeof(float));
+  L.part = 0;
+  const size_t slot = decode_part_floats(rows, int(head_dim)) * sizeof(float);
+  L.warp_part = L.part + align_up(size_t(ctas) * 2 * slot);
+  L.total = L.warp_part + align_up(size_t(ctas) * kDecodeWarps * slot);
   return L;
 }
 
@@ -192,7 +192,7 @@ fa_status fa_paged_decode_workspace_size(int64_t batch, int64_t head_num, int64_
   const fa_status st = check_heads(head_num, head_num_kv, head_dim, dtype);
   if (st != FA_OK) return st;
   const int rows = decode_rows(dtype, int(head_num / head_num_kv));
-  *workspace_bytes = decode_layout(sm_count() * kDecodeCtasPerSm, rows, head_dim).total;
+  *workspace_bytes = decode_layout(sm_count(), rows, head_dim).total;
   return FA_OK;
 }
 
@@ -222,8 +222,7 @@ fa_status fa_paged_decode(const void *q, int64_t q_stride, const void *k_pages,
   if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return FA_ERR_INVALID;
   const int sms = sm_count();
   const int group = int(head_num / head_num_kv);
-  const DecodeLayout L =
-      decode_layout(sms * kDecodeCtasPerSm, decode_rows(dtype, group), head_dim);
+  const DecodeLayout L = decode_layout(sms, decode_rows(dtype, group), head_dim);
   if (workspace_bytes < L.total) return FA_ERR_WORKSPACE;
 
   DecodeParams p{};
@@ -242,8 +241,8 @@ fa_status fa_paged_decode(const void *q, int64_t q_stride, const void *k_pages,
   p.smax = softmax_max;
   p.ssum = softmax_sum;
   p.error = error;
-  p.meta = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + L.meta);
   p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.part);
+  p.warp_part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.warp_part);
   p.num_pages = int(num_pages);
   p.page_size = int(page_size);
   p.page_shift = -1;
@@ -257,6 +256,11 @@ fa_status fa_paged_decode(const void *q, int64_t q_stride, const void *k_pages,
   p.n_kv = int(head_num_kv);
   p.d = int(head_dim);
   p.group = group;
+  const auto pairs = [](const void *ptr, int64_t stride) {
+    return reinterpret_cast<uintptr_t>(ptr) % 4 == 0 && stride % 2 == 0;
+  };
+  p.q_pairs = pairs(q, q_stride);
+  p.y_pairs = pairs(y, y_stride);
   p.pre = int(pre_tokens < -1 ? -1 : pre_tokens > kMaxKeys ? kMaxKeys : pre_tokens);
   p.scale = float(scale);
   p.scale_log2 = float(scale * 1.4426950408889634);

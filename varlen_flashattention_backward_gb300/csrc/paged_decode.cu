@@ -13,29 +13,28 @@ namespace fav {
 namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-// A segment costs a CTA about this many blocks of keys beside its own.
-constexpr int kSwitchBlocks = 2;
+constexpr uint32_t kFull = 0xffffffffu;
+// Beginning a segment costs a warp about as much as this many blocks of keys.
+constexpr int kSwitchBlocks = 1;
 
 // ---------------------------------------------------------------------------
 // Division of the work
 //
 // A segment is one request, one key head and up to R of its query heads; its
-// keys are cut into blocks of KB.  The segments, each weighing its blocks plus
-// kSwitchBlocks, form a line that is cut into `grid` ranges of equal weight,
-// one per CTA.  A CTA's share of a segment is a part.  A part that is a whole
-// segment writes y; of the others a CTA has at most two (its first and its
-// last), which go to its two slots of the workspace: slot 0 for a part that
-// does not begin its segment, slot 1 for one that begins it and does not end
-// it.  join_kernel adds the parts of a segment in order.
+// keys are cut into blocks of KB (at least one, which may hold no key).  The
+// segments, each weighing its blocks plus kSwitchBlocks, form a line that is
+// cut into ranges of equal weight, one per warp of the grid.  Weights count in
+// units of 2^unit_shift blocks, which the host chooses so that 32 bits hold the
+// line's length; the shift is 0 for any batch that fits a GPU's memory.
+//
+// A warp's share of a segment is a part.  A part that is a whole segment
+// writes y from the warp's registers.  Of the others a warp has at most two,
+// its first (slot A, where it does not begin its segment) and its last (slot B,
+// where it does); they wait until the CTA's warps are done, when neighbouring
+// parts of one segment are added.  What then still misses a neighbour, at most
+// two sums per CTA, goes to the workspace: slot 0 where it does not begin its
+// segment, slot 1 where it does.  join_kernel adds those, in order.
 // ---------------------------------------------------------------------------
-struct Part {
-  int b, seg;        // request; segment index inside the request
-  int first, last;   // blocks [first, last), relative to the segment's first
-  int blocks;        // of the whole segment
-};
-
 struct Span {
   int lo, hi;        // keys [lo, hi) that the query sees
   int blk0;          // first block (absolute)
@@ -43,113 +42,277 @@ struct Span {
 };
 
 template <int KB>
-__device__ __forceinline__ Span span_of(const DecodeParams &p, int b) {
+__device__ __forceinline__ Span span_of(const DecodeParams &p, int len) {
   Span s;
   const int most = p.max_pages * p.page_size;
-  int len = p.lens[b];
   len = len < 0 ? 0 : len > most ? most : len;
   s.hi = len;
   const int lo = len - 1 - p.pre;
   s.lo = lo < 0 ? 0 : lo > len ? len : lo;
   s.blk0 = s.lo / KB;
-  s.blocks = s.hi > s.lo ? (s.hi + KB - 1) / KB - s.blk0 : 0;
+  s.blocks = s.hi > s.lo ? (s.hi + KB - 1) / KB - s.blk0 : 1;
   return s;
 }
 
-// Walks the parts of one CTA's range in order.
-template <int KB>
-struct Walk {
-  int64_t left;      // weight left of the range
-  int off;           // weight already passed inside the current segment
-  int b, seg, segs;
-  Span span;         // of request b
-  Span part_span;    // of the part that next() gave
+__device__ __forceinline__ int units_of(const DecodeParams &p, int blocks) {
+  return (blocks + kSwitchBlocks + (1 << p.unit_shift) - 1) >> p.unit_shift;
+}
 
-  __device__ __forceinline__ bool next(const DecodeParams &p, Part &part) {
-    while (left > 0) {
-      const int weight = span.blocks + kSwitchBlocks;
-      const int end = int(min(off + left, int64_t(weight)));
-      part.b = b;
-      part.seg = seg;
-      part.blocks = span.blocks;
-      part.first = max(off - kSwitchBlocks, 0);
-      part.last = max(end - kSwitchBlocks, 0);
-      part_span = span;
-      const bool opens = off == 0;
-      left -= end - off;
-      off = end;
-      if (end == weight) {
-        off = 0;
-        if (++seg == segs) {
-          seg = 0;
-          if (++b < p.batch && left > 0) span = span_of<KB>(p, b);
-        }
-      }
-      if (part.last > part.first || (part.blocks == 0 && opens)) return true;
-    }
-    return false;
+// The line: its ranges' lengths (the first `rest` are one longer than `each`).
+struct Line {
+  int each, rest;
+  __device__ __forceinline__ int start(int range) const {
+    return range * each + min(range, rest);
+  }
+  __device__ __forceinline__ int range_of(int unit) const {
+    const int longer = rest * (each + 1);
+    return unit < longer ? unit / (each + 1) : rest + (unit - longer) / each;
   }
 };
 
-// Places `w` at the start of the CTA's range.  All threads of the CTA call it.
+// A place on it: a segment, and how far inside.
+struct Place {
+  int b, seg;        // request, segment inside it
+  int off;           // units into the segment
+  int units;         // of each of the request's segments
+};
+
+// Measures the line and finds unit `start(range)` on it.  Every warp that asks
+// works it out for itself from all lengths, a lane taking a 32nd of them: that
+// costs less than meeting other warps would.  False: nothing is there.
 template <int KB>
-__device__ void place(const DecodeParams &p, int segs, Walk<KB> &w) {
-  __shared__ int64_t s_sum[kWarps];
-  __shared__ int64_t s_off;
-  __shared__ int s_b;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.batch + kThreads - 1) / kThreads;
-  const int b0 = tid * per, b1 = min(b0 + per, p.batch);
+__device__ __forceinline__ bool find(const DecodeParams &p, int segs, int range, int before,
+                                     Line &line, Place &at) {
+  const int lane = threadIdx.x & 31;
+  const int per = (p.batch + 31) >> 5;
+  const int b0 = lane * per;
   const int most = p.max_pages * p.page_size;
-  int64_t sum = 0;
+  int sum = 0, units = 0;
   bool bad = false;
-  for (int b = b0; b < b1; ++b) {
-    sum += int64_t(span_of<KB>(p, b).blocks + kSwitchBlocks) * segs;
-    const int len = p.lens[b];
-    bad |= len < 0 || len > most;
-  }
-  if (bad && blockIdx.x == 0 && p.error) atomicOr(p.error, FA_PAGED_BAD_LENGTH);
-  int64_t x = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) s_sum[warp] = x;
-  __syncthreads();
-  int64_t before = x - sum, total = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < warp) before += s_sum[i];
-    total += s_sum[i];
-  }
-  // Ranges differ by at most one block of weight.
-  const int64_t each = total / p.grid, rest = total % p.grid;
-  const int64_t i = blockIdx.x;
-  const int64_t u0 = i * each + min(i, rest);
-  w.left = each + (i < rest ? 1 : 0);
-  if (w.left > 0 && u0 >= before && u0 < before + sum) {
-    int64_t at = before;
-    for (int b = b0; b < b1; ++b) {
-      const int64_t mine = int64_t(span_of<KB>(p, b).blocks + kSwitchBlocks) * segs;
-      if (u0 < at + mine) {
-        s_b = b;
-        s_off = u0 - at;
-        break;
-      }
-      at += mine;
+#pragma unroll 4
+  for (int i = 0; i < per; ++i) {
+    if (b0 + i < p.batch) {
+      const int len = __ldg(p.lens + b0 + i);
+      bad |= len < 0 || len > most;
+      units = units_of(p, span_of<KB>(p, len).blocks);
+      sum += units;
     }
   }
-  __syncthreads();
-  w.segs = segs;
-  if (w.left > 0) {
-    w.b = s_b;
-    w.span = span_of<KB>(p, w.b);
-    const int64_t weight = w.span.blocks + kSwitchBlocks;
-    w.seg = int(s_off / weight);
-    w.off = int(s_off - w.seg * weight);
+  if (bad && range == 0 && p.error) atomicOr(p.error, FA_PAGED_BAD_LENGTH);
+  sum *= segs;
+  int upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, upto, o);
+    if (lane >= o) upto += y;
   }
+  const int total = __shfl_sync(kFull, upto, 31);
+  line.each = total / p.ranges;
+  line.rest = total - line.each * p.ranges;
+  const int u = line.start(range) - before;
+  if (u < 0 || u >= total) return false;
+  // The lane, then the request, inside which u falls.
+  const int owner = __popc(__ballot_sync(kFull, upto <= u));
+  int from = __shfl_sync(kFull, upto - sum, owner);
+  at.b = owner * per;
+  at.units = __shfl_sync(kFull, units, owner);
+  if (per > 1) {
+    for (int i = 0; i < per; i += 32) {
+      const int b = owner * per + i + lane;
+      const int w = i + lane < per && b < p.batch
+                        ? units_of(p, span_of<KB>(p, __ldg(p.lens + b)).blocks)
+                        : 0;
+      int x = w * segs;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, x, o);
+        if (lane >= o) x += y;
+      }
+      const int n = __popc(__ballot_sync(kFull, from + x <= u));
+      if (n < 32) {
+        at.b = owner * per + i + n;
+        at.units = __shfl_sync(kFull, w, n);
+        from += __shfl_sync(kFull, x, n) - at.units * segs;
+        break;
+      }
+      from += __shfl_sync(kFull, x, 31);
+    }
+  }
+  at.seg = (u - from) / at.units;
+  at.off = u - from - at.seg * at.units;
+  return true;
 }
+
+// Measures the line and gives the first unit of segment (at.b, at.seg), whose
+// units it fills in.
+template <int KB>
+__device__ __forceinline__ int segment_start(const DecodeParams &p, int segs, Place &at,
+                                             Line &line) {
+  int sum = 0, before = 0;
+  for (int b = threadIdx.x & 31; b < p.batch; b += 32) {
+    const int units = units_of(p, span_of<KB>(p, __ldg(p.lens + b)).blocks);
+    sum += units;
+    if (b < at.b) before += units;
+  }
+  const int total = __reduce_add_sync(kFull, sum) * segs;
+  line.each = total / p.ranges;
+  line.rest = total - line.each * p.ranges;
+  at.units = units_of(p, span_of<KB>(p, __ldg(p.lens + at.b)).blocks);
+  at.off = 0;
+  return __reduce_add_sync(kFull, before) * segs + at.seg * at.units;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(take ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// What a block in the ring is: x = mask of its keys | flags << 16, y = request,
+// z = segment inside the request.
+enum : int {
+  kPartBegins = 1 << 16,   // first block of a part
+  kPartEnds = 1 << 17,
+  kSegBegins = 1 << 18,    // first block of a segment
+  kSegEnds = 1 << 19,
+  kRangeEnds = 1 << 20,    // last block of the warp's range
+  kDone = 1 << 21          // no block: the range is done
+};
+
+// Shared memory of one kernel: NW rings of S stages (K and V block each), then
+// what the kernel adds per warp.  Three stages of eight warps keep 128 KB on
+// the way, which is what the memory needs; where they do not fit, four warps
+// with more stages are taken if they do better (MINS: the stages that eight
+// warps must have).
+template <typename T, int D, int R, int KB, int EXTRA, int MINS>
+struct Shape {
+  static constexpr int PAD = 4;
+  static constexpr int kBlock = KB * D * int(sizeof(T));      // K or V block of one warp
+  static constexpr int kStage = 2 * kBlock;
+  static constexpr int kPartial = R * (D + PAD) * 4;
+  static constexpr int kExtra = EXTRA;
+  static constexpr int kBudget = 227 * 1024 - 4096;           // 4 KB of static arrays
+  static constexpr int fit(int nw) { return (kBudget - nw * kExtra) / (nw * kStage); }
+  static constexpr int NW = fit(8) >= MINS ? 8 : 4;
+  static constexpr int S = fit(NW) > 8 ? 8 : fit(NW);
+  static constexpr int kSmem = NW * (S * kStage + kExtra);
+  static_assert(S >= 2 && S * kStage >= kPartial, "decode stages");
+};
+
+// The loading side of a warp: walks its range and keeps the ring filled.
+// `look` finds the next block and starts the load of its page ids; `issue`,
+// one block later, uses them to start the copies of its rows.
+template <typename T, int D, int KB, int S, typename Swizzle>
+struct Loader {
+  static constexpr int VEC = 16 / int(sizeof(T));
+  static constexpr int CPR = D / VEC;              // 16-byte chunks per row
+  static constexpr int kLoads = KB * CPR / 32;     // chunks per lane, K or V
+  static_assert(KB * CPR % 32 == 0 && KB <= 16, "decode block");
+  const DecodeParams &p;
+  const int chunks, segs, lane;
+  int left;                      // units left of the range
+  int off, units, b, seg;        // units into the segment, and of it
+  int blk, end;                  // next block of the part, and its end
+  bool begins;                   // blk begins its part
+  Span span;
+  int4 desc;
+  int page, tok, head, err;
+  bool inside;
+
+  __device__ __forceinline__ Loader(const DecodeParams &p, int range, int chunks)
+      : p(p), chunks(chunks), segs(p.n_kv * chunks), lane(threadIdx.x & 31), left(0), off(0),
+        units(0), b(0), seg(0), blk(0), end(0), begins(false), page(-1), tok(0), head(0), err(0),
+        inside(false) {
+    Line line;
+    Place at;
+    if (find<KB>(p, segs, range, 0, line, at)) {
+      left = line.each + (range < line.rest ? 1 : 0);
+      b = at.b;
+      seg = at.seg;
+      off = at.off;
+      enter();
+    }
+  }
+
+  // Request b's span (its segments have the same).
+  __device__ __forceinline__ void enter() {
+    span = span_of<KB>(p, __ldg(p.lens + b));
+    units = units_of(p, span.blocks);
+  }
+
+  __device__ __forceinline__ void look() {
+    while (blk >= end) {
+      if (left <= 0) {
+        desc.x = kDone;
+        return;
+      }
+      // The next part: the rest of the range inside the current segment.
+      const int upto = min(off + left, units);
+      blk = max((off << p.unit_shift) - kSwitchBlocks, 0);
+      end = min((upto << p.unit_shift) - kSwitchBlocks, span.blocks);
+      begins = true;
+      left -= upto - off;
+      off = upto;
+      if (blk >= end) continue;    // all of it is the segment's beginning
+      desc.y = b;
+      desc.z = seg;
+      head = chunks == 1 ? seg : seg / chunks;
+    }
+    const int j = (span.blk0 + blk) * KB + (lane % KB);
+    inside = j >= span.lo && j < span.hi;
+    if (inside) {
+      const int idx = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
+      tok = j - idx * p.page_size;
+      page = p.table[desc.y * p.table_stride + idx];
+    }
+    desc.x = (begins ? kPartBegins : 0) | (blk == 0 ? kSegBegins : 0);
+    begins = false;
+    if (++blk >= end) {
+      desc.x |= kPartEnds | (end == span.blocks ? kSegEnds : 0) | (left == 0 ? kRangeEnds : 0);
+      if (off == units) {          // on to the next segment
+        off = 0;
+        if (++seg == segs) {
+          seg = 0;
+          if (++b < p.batch && left > 0) enter();
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void issue(uint32_t dst, int4 *at) {
+    if (!(desc.x & kDone)) {
+      int64_t o = -1;
+      if (inside) {
+        if (page >= 0 && page < p.num_pages)
+          o = page * p.page_stride + tok * p.token_stride + head * p.head_stride;
+        else
+          err = FA_PAGED_BAD_PAGE;
+      }
+      const uint32_t mask = __ballot_sync(kFull, o >= 0) & ((1u << KB) - 1);
+      if (lane == 0) *at = make_int4(desc.x | int(mask), desc.y, desc.z, 0);
+      const T *kc = static_cast<const T *>(p.kc), *vc = static_cast<const T *>(p.vc);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int c = i * 32 + lane, r = c / CPR, ch = c % CPR;
+        const int64_t row = __shfl_sync(kFull, o, r);
+        const uint32_t to = dst + (r * CPR + (ch ^ Swizzle::at(r))) * 16;
+        const int64_t from = (row < 0 ? 0 : row) + ch * VEC;
+        cp_async16(to, kc + from, row >= 0);
+        cp_async16(to + KB * CPR * 16, vc + from, row >= 0);
+      }
+    } else if (lane == 0) {
+      *at = make_int4(kDone, 0, 0, 0);
+    }
+    cp_async_commit();
+  }
+};
 
 // Floats of one workspace slot: o [rows][d], then the rows' maxima and sums.
 __host__ __device__ constexpr int slot_floats(int rows, int d) { return rows * (d + 4); }
@@ -169,63 +332,107 @@ __device__ __forceinline__ void write_stats(const DecodeParams &p, int b, int n,
   }
 }
 
-// What a CTA's parts left in the workspace, four words per CTA: the segment
-// (b * segs + seg) whose part is in slot 0 (or -1), whether that part ends it,
-// the segment in slot 1 (or -1).
-struct Meta {
-  int seg0 = -1, ends0 = 0, seg1 = -1;
-  __device__ __forceinline__ void note(const Part &part, int segs) {
-    const int id = part.b * segs + part.seg;
-    if (part.first == 0) {
-      seg1 = id;
-    } else {
-      seg0 = id;
-      ends0 = part.last == part.blocks;
-    }
-  }
-  __device__ __forceinline__ void store(const DecodeParams &p) const {
-    *reinterpret_cast<int4 *>(p.meta + blockIdx.x * 4) = make_int4(seg0, ends0, seg1, 0);
-  }
+// The partial results of a CTA's warps: slot A of the part that does not begin
+// its segment, slot B of the part that does and does not end it.
+template <int NW, int R>
+struct Partials {
+  float m[2][NW][R], l[2][NW][R];
+  const float *o[2][NW];            // [R][D + PAD]
+  int id[2][NW];                    // segment (b * segs + seg), or -1
+  int ends[2][NW];                  // whether the part ends it
 };
 
-// The end of a part: the warps' maxima, sums and outputs in shared memory
-// (o [warp][row][D + pad]) become y and the statistics, or a workspace slot.
-// Four dims per thread.
-template <typename T, int D, int R, int PAD>
-__device__ __forceinline__ void finish_part(const DecodeParams &p, const Part &part, int n0,
-                                            int heads, const float *s_o, const float *s_m,
-                                            const float *s_l) {
-  const bool whole = part.first == 0 && part.last == part.blocks;
-  float *dst = slot_of(p, blockIdx.x, part.first == 0 ? 1 : 0, R);
-  for (int i = threadIdx.x; i < heads * (D / 4); i += kThreads) {
-    const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
-    float mx = -CUDART_INF_F;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) mx = fmaxf(mx, s_m[k * R + r]);
-    const float ref = mx == -CUDART_INF_F ? 0.f : mx;
-    float sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      const float f = exp2f(s_m[k * R + r] - ref);
-      const float4 o = *reinterpret_cast<const float4 *>(s_o + (k * R + r) * (D + PAD) + d);
-      sum += f * s_l[k * R + r];
-      acc.x += f * o.x;
-      acc.y += f * o.y;
-      acc.z += f * o.z;
-      acc.w += f * o.w;
+// Where a warp puts the partial result of a part: its ring when the part is
+// the last of its range (nothing is on the way behind it), else, so for a slot A
+// that more parts follow, its place in the workspace.
+template <int NW>
+__device__ __forceinline__ float *partial_at(const DecodeParams &p, int rows, bool last,
+                                             const uint8_t *ring) {
+  if (last) return reinterpret_cast<float *>(const_cast<uint8_t *>(ring));
+  return p.warp_part +
+         (int64_t(blockIdx.x) * NW + (threadIdx.x >> 5)) * slot_floats(rows, p.d);
+}
+
+// Adds neighbouring partial results (see the top) once every warp is done.
+// Run 0 begins with warp 0's slot A, run 1 + w with warp w's slot B; a run
+// goes on with the slots A of the warps behind it.  A warp takes one row of
+// one run at a time.
+template <typename T, int D, int R, int NW, int PAD>
+__device__ __forceinline__ void merge_partials(const DecodeParams &p, int chunks,
+                                               const Partials<NW, R> &s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = min(R, p.group);
+  // Lane k < NW: the id in warp k's slot A, lane 16 + k: in its slot B.
+  const int id_of = (lane & 15) < NW ? s.id[lane >> 4][lane & 15] : -1;
+  const uint32_t held = __ballot_sync(kFull, id_of >= 0);
+  // Runs begin at warp 0's slot A and at every slot B.
+  uint32_t runs = held & 0xffff0001u;
+  const int tasks = __popc(runs) * rows;
+#pragma unroll 1
+  for (int task = warp; task < tasks; task += NW) {
+    const int run = task / rows, r = task - run * rows;
+    uint32_t rest = runs;
+    for (int i = 0; i < run; ++i) rest &= rest - 1;
+    const int at = __ffs(rest) - 1, slot = at >> 4, w0 = at & 15;
+    // Its members: w0, then the slots A behind it up to the first gap or the
+    // first that ends the segment.
+    int count = 1;
+    bool ends = s.ends[slot][w0];
+    while (!ends && w0 + count < NW) {
+      ends = s.ends[0][w0 + count];
+      ++count;
     }
-    if (whole) {
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      T *y = static_cast<T *>(p.y) + part.b * p.y_stride + int64_t(n0 + r) * D + d;
-      y[0] = from_f<T>(acc.x * inv);
-      y[1] = from_f<T>(acc.y * inv);
-      y[2] = from_f<T>(acc.z * inv);
-      y[3] = from_f<T>(acc.w * inv);
-      if (d == 0) write_stats(p, part.b, n0 + r, mx * kLn2, sum);
-    } else {
-      *reinterpret_cast<float4 *>(dst + r * D + d) = acc;
-      if (d == 0) {
+    const int id = __shfl_sync(kFull, id_of, at);
+    const int segs = p.n_kv * chunks;
+    const int b = id / segs, seg = id - b * segs;
+    const int h = (chunks == 1 ? 0 : seg % chunks * R) + r;
+    if (h >= p.group) continue;
+    const int n = (chunks == 1 ? seg : seg / chunks) * p.group + h;
+    const int mine = lane < count ? lane : 0;
+    const int my_slot = mine == 0 ? slot : 0;
+    const float m = s.m[my_slot][w0 + mine][r], l = s.l[my_slot][w0 + mine][r];
+    float mx = m;
+#pragma unroll
+    for (int o = 1; o < NW; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    const float f = sm103::ex2(m - (mx == -CUDART_INF_F ? 0.f : mx));
+    float sum = 0.f;
+    const bool whole = slot == 1 && ends;
+    float *dst = slot_of(p, blockIdx.x, slot, R);
+#pragma unroll
+    for (int d0 = 0; d0 < D; d0 += 128) {
+      const int d = d0 + lane * 4;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      sum = 0.f;
+#pragma unroll 2
+      for (int k = 0; k < count; ++k) {
+        const float fk = __shfl_sync(kFull, f, k);
+        sum += fk * __shfl_sync(kFull, l, k);
+        if (d < D) {
+          const float4 o = *reinterpret_cast<const float4 *>(
+              s.o[k == 0 ? slot : 0][w0 + k] + r * (D + PAD) + d);
+          acc.x += fk * o.x;
+          acc.y += fk * o.y;
+          acc.z += fk * o.z;
+          acc.w += fk * o.w;
+        }
+      }
+      if (d < D) {
+        if (whole) {
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          T *y = static_cast<T *>(p.y) + b * p.y_stride + int64_t(n) * D + d;
+          y[0] = from_f<T>(acc.x * inv);
+          y[1] = from_f<T>(acc.y * inv);
+          y[2] = from_f<T>(acc.z * inv);
+          y[3] = from_f<T>(acc.w * inv);
+        } else {
+          *reinterpret_cast<float4 *>(dst + r * D + d) = acc;
+        }
+      }
+    }
+    if (lane == 0) {
+      if (whole) {
+        write_stats(p, b, n, mx * kLn2, sum);
+      } else {
         dst[R * D + r] = mx;
         dst[R * D + R + r] = sum;
       }
@@ -233,28 +440,9 @@ __device__ __forceinline__ void finish_part(const DecodeParams &p, const Part &p
   }
 }
 
-// Page of key j of request b, or -1 (with `bad` set) where its id is none.
-__device__ __forceinline__ int page_of(const DecodeParams &p, int j, int &in_page) {
-  const int idx = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
-  in_page = j - idx * p.page_size;
-  return idx;
-}
-
 // ---------------------------------------------------------------------------
 // Tensor-core kernel, 16-bit types
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool take) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(take ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -294,24 +482,22 @@ __device__ __forceinline__ float2 unpack2(uint32_t x) {
   return make_float2(to_f(h[0]), to_f(h[1]));
 }
 
-template <int D, int R>
-struct TcShape {
-  static constexpr int KB = 16;
-  static constexpr int PAD = 4;
-  static constexpr int kCtas = D <= 128 ? 2 : 1;            // per SM
-  static constexpr int kStageBytes = KB * D * 2 * 2;        // one warp's K and V block
-  static constexpr int kMergeBytes = kWarps * R * (D + PAD) * 4;
-  static constexpr int kBudget = (kCtas == 2 ? 114 : 227) * 1024 - 2048;
-  static constexpr int kFit = (kBudget - kMergeBytes) / (kWarps * kStageBytes);
-  static constexpr int kStages = kFit > 8 ? 8 : kFit;
-  static constexpr int kSmem = kStages * kWarps * kStageBytes + kMergeBytes;
-  static_assert(kStages >= 2, "decode stages");
+// Row r's chunk c of a block sits at chunk c ^ at(r) of the row, so that the
+// eight rows of an 8x8 matrix fall into different banks (rows are an odd
+// multiple of 64 bytes where CPR % 8 != 0).
+template <int CPR>
+struct TcSwizzle {
+  static __device__ __forceinline__ int at(int r) {
+    return CPR % 8 == 0 ? (r & 7) : ((r >> 1) & 3);
+  }
 };
+
+template <int D, int R>
+using TcShape = Shape<__half, D, R, 16, 0, 2>;
 
 // S = Q K^T and O = P V by m16n8k16 products: Q's rows are the group's query
 // heads, padded to 16, and a warp takes 16 keys at a time through its own ring
-// of stages, filled by cp.async ahead of use.  Warps meet only at the end of a
-// part.
+// of stages, filled by cp.async ahead of use.
 //
 // P goes into the second product as the sum of two 16-bit numbers, so that
 // its rounding (2^-17 for bf16) stays below y's own.  With R = 8 the two
@@ -319,419 +505,491 @@ struct TcShape {
 // of it, and the halves of the result are added at the end.  With R = 16 they
 // are two products.
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(kThreads, TcShape<D, R>::kCtas)
+__global__ void __launch_bounds__(TcShape<D, R>::NW * 32, 1)
 decode_tc_kernel(const __grid_constant__ DecodeParams p) {
   using Sh = TcShape<D, R>;
-  constexpr int KB = Sh::KB, S = Sh::kStages;
-  constexpr int CPR = D / 8;                       // 16-byte chunks per row
-  constexpr int kLoads = KB * CPR / 32;            // chunks per lane, K or V
+  using Sw = TcSwizzle<D / 8>;
+  constexpr int KB = 16, S = Sh::S, NW = Sh::NW;
+  constexpr int CPR = D / 8;
+  constexpr int NR = R / 8;         // rows of a lane
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ float s_m[kWarps * R], s_l[kWarps * R];
-  __shared__ uint32_t s_mask[kWarps][S];
+  __shared__ Partials<NW, R> s_part;
+  __shared__ int4 s_desc[NW][S];
   asm volatile("griddepcontrol.launch_dependents;");
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  float *s_o = reinterpret_cast<float *>(smem + S * kWarps * Sh::kStageBytes);
-  const uint32_t ring = sm103::smem_u32(smem) + warp * S * Sh::kStageBytes;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint8_t *my = smem + warp * S * Sh::kStage;
+  const uint32_t ring = sm103::smem_u32(my);
   const T *q = static_cast<const T *>(p.q);
-  const T *kc = static_cast<const T *>(p.kc), *vc = static_cast<const T *>(p.vc);
-  const int chunks = (p.group + R - 1) / R;
+  const int chunks = (p.group + R - 1) / R, segs = p.n_kv * chunks;
+  if (lane < 2) s_part.id[lane][warp] = -1;
 
-  Walk<KB> w;
-  place<KB>(p, p.n_kv * chunks, w);
-
-  // Row r's chunk c of a block sits at chunk c ^ swizzle(r) of the row, so that
-  // the eight rows of an 8x8 matrix fall into different banks.
-  auto swizzle = [](int r) { return CPR % 8 == 0 ? (r & 7) : ((r >> 1) & 3); };
-
-  // --- The loading side: `look` finds the next block and loads its page ids
-  // one block ahead of `issue`, which starts the copies.
-  Walk<KB> pw = w;
-  Part pp;
-  pp.last = 0;
-  int p_blk = 0;
-  int nx_j = 0, nx_page = -1, nx_tok = 0, nx_head = 0;
-  bool nx_any = true, nx_in = false;
-  int err = 0;
-  auto look = [&]() {
-    while (nx_any && p_blk >= pp.last) {
-      nx_any = pw.next(p, pp);
-      p_blk = nx_any ? pp.first + warp : 0;
-    }
-    nx_in = false;
-    if (!nx_any) return;
-    const Span &sp = pw.part_span;
-    nx_j = (sp.blk0 + p_blk) * KB + (lane & 15);
-    nx_head = pp.seg / chunks;
-    nx_in = nx_j >= sp.lo && nx_j < sp.hi;
-    if (nx_in) nx_page = p.table[pp.b * p.table_stride + page_of(p, nx_j, nx_tok)];
-    p_blk += kWarps;
-  };
-  auto issue = [&](int stage) {
-    if (nx_any) {
-      int64_t off = -1;
-      if (nx_in) {
-        if (nx_page >= 0 && nx_page < p.num_pages)
-          off = nx_page * p.page_stride + nx_tok * p.token_stride + nx_head * p.head_stride;
-        else
-          err = FA_PAGED_BAD_PAGE;
-      }
-      const uint32_t mask = __ballot_sync(0xffffffffu, off >= 0) & 0xffffu;
-      if (lane == 0) s_mask[warp][stage] = mask;
-      const uint32_t dst = ring + stage * Sh::kStageBytes;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int c = i * 32 + lane, r = c / CPR, ch = c % CPR;
-        const int64_t o = __shfl_sync(0xffffffffu, off, r);
-        const uint32_t to = dst + (r * CPR + (ch ^ swizzle(r))) * 16;
-        const int64_t from = (o < 0 ? 0 : o) + ch * 8;
-        cp_async16(to, kc + from, o >= 0);
-        cp_async16(to + KB * D * 2, vc + from, o >= 0);
-      }
-    }
-    cp_async_commit();
-  };
-
-  look();
+  Loader<T, D, KB, S, Sw> load(p, blockIdx.x * NW + warp, chunks);
+  load.look();
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) {
-    issue(i);
-    look();
+    load.issue(ring + i * Sh::kStage, &s_desc[warp][i]);
+    load.look();
   }
 
-  // --- The computing side.
   const int row = lane >> 2, col = (lane & 3) * 2;
   // ldmatrix addresses inside a block: K (n = key, k = dim) and V (transposed).
   const int k_row = (lane & 7) + ((lane >> 4) << 3), k_ch = (lane >> 3) & 1;
   const int v_row = (lane & 7) + (((lane >> 3) & 1) << 3), v_ch = lane >> 4;
-  int stage = 0, fill = S - 1;
-  Meta meta;
-  Part part;
-  while (w.next(p, part)) {
-    const int hk = part.seg / chunks, h0 = (part.seg % chunks) * R;
-    const int heads = min(R, p.group - h0), n0 = hk * p.group + h0;
-    uint32_t qa[D / 16][R == 8 ? 2 : 4];
-    {
-      const T *qr = q + part.b * p.q_stride + int64_t(n0) * D;
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-        for (int i = 0; i < (R == 8 ? 2 : 4); ++i) {
-          const int r = R == 8 ? row : row + (i & 1) * 8;
-          const int d = ks * 16 + col + (R == 8 ? i : i >> 1) * 8;
-          uint32_t x = 0;
-          if (r < heads) {
-            T *h = reinterpret_cast<T *>(&x);
-            h[0] = qr[r * D + d];
-            h[1] = qr[r * D + d + 1];
-          }
-          qa[ks][i] = x;
-        }
-    }
-    float o[D / 8][4];
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
-    constexpr int NR = R / 8;       // rows of a lane
-    float m[NR], l[NR];
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      m[i] = -CUDART_INF_F;
-      l[i] = 0.f;
-    }
+  int stage = 0, fill = S - 1, heads = 0, n0 = 0;
+  uint32_t qa[D / 16][2 * NR];
+  float o[D / 8][4];
+  float m[NR], l[NR];
+  bool opens = false;
 
 #pragma unroll 1
-    for (int blk = part.first + warp; blk < part.last; blk += kWarps) {
-      cp_async_wait<S - 2>();
-      __syncwarp();
-      const uint32_t kb = ring + stage * Sh::kStageBytes, vb = kb + KB * D * 2;
-      const uint32_t mask = s_mask[warp][stage];
-      issue(fill);
-      look();
-      fill = fill + 1 == S ? 0 : fill + 1;
-      stage = stage + 1 == S ? 0 : stage + 1;
+  while (true) {
+    cp_async_wait<S - 2>();
+    __syncwarp();
+    const int4 desc = s_desc[warp][stage];
+    if (desc.x & kDone) break;
+    const uint32_t kb = ring + stage * Sh::kStage, vb = kb + Sh::kBlock;
+    load.issue(ring + fill * Sh::kStage, &s_desc[warp][fill]);
+    load.look();
+    fill = fill + 1 == S ? 0 : fill + 1;
+    stage = stage + 1 == S ? 0 : stage + 1;
 
-      float sa[2][2][4];            // [chain][key half][fragment]
+    if (desc.x & kPartBegins) {
+      const int hk = desc.z / chunks, h0 = (desc.z - hk * chunks) * R;
+      heads = min(R, p.group - h0);
+      n0 = hk * p.group + h0;
+      opens = desc.x & kSegBegins;
+      const T *qr = q + desc.y * p.q_stride + int64_t(n0) * D;
+      // Fragment i of a step: rows row (and row + 8 for odd i with R = 16).  Rows
+      // behind the last head repeat it; nothing reads their results.
 #pragma unroll
-      for (int i = 0; i < 16; ++i) (&sa[0][0][0])[i] = 0.f;
+      for (int i = 0; i < 2 * NR; ++i) {
+        const int r = min(row + (NR == 2 ? (i & 1) * 8 : 0), heads - 1);
+        const T *src = qr + r * D + col + (NR == 2 ? i >> 1 : i) * 8;
+        if (p.q_pairs) {
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t kf[4];
-        ldsm4(kf, kb + (k_row * CPR + ((ks * 2 + k_ch) ^ swizzle(k_row))) * 16);
-        uint32_t a[4];
-        if constexpr (R == 8) {
-          a[0] = qa[ks][0];
-          a[1] = 0;
-          a[2] = qa[ks][1];
-          a[3] = 0;
+          for (int ks = 0; ks < D / 16; ++ks)
+            qa[ks][i] = __ldg(reinterpret_cast<const uint32_t *>(src + ks * 16));
         } else {
+          const uint16_t *h = reinterpret_cast<const uint16_t *>(src);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) a[i] = qa[ks][i];
+          for (int ks = 0; ks < D / 16; ++ks)
+            qa[ks][i] = uint32_t(h[ks * 16]) | uint32_t(h[ks * 16 + 1]) << 16;
         }
-        mma16816<T>(sa[ks & 1][0], a, kf[0], kf[1]);
-        mma16816<T>(sa[ks & 1][1], a, kf[2], kf[3]);
       }
-      float s[NR][4];               // keys col, col + 1, col + 8, col + 9
-      float mn[NR];
-      bool grows = false;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
-        float t = -CUDART_INF_F;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = col + (e & 1) + (e >> 1) * 8;
-          const float x = (sa[0][e >> 1][i * 2 + (e & 1)] + sa[1][e >> 1][i * 2 + (e & 1)]) *
-                          p.scale_log2;
-          s[i][e] = (mask >> key) & 1 ? x : -CUDART_INF_F;
-          t = fmaxf(t, s[i][e]);
-        }
-        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-        mn[i] = fmaxf(m[i], t);
-        grows |= mn[i] > m[i];
+        m[i] = -CUDART_INF_F;
+        l[i] = 0.f;
       }
-      if (__any_sync(0xffffffffu, grows)) {
+    }
+
+    float sa[2][2][4];              // [chain][key half][fragment]
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          // m = -inf here means that o and l are 0 (or NaN) still.
-          const float f = m[i] == mn[i] ? 1.f : sm103::ex2(m[i] - mn[i]);
-          m[i] = mn[i];
-          l[i] *= f;
+    for (int i = 0; i < 16; ++i) (&sa[0][0][0])[i] = 0.f;
 #pragma unroll
-          for (int k = 0; k < D / 8; ++k) {
-            if constexpr (R == 8) {
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint32_t kf[4];
+      ldsm4(kf, kb + (k_row * CPR + ((ks * 2 + k_ch) ^ Sw::at(k_row))) * 16);
+      uint32_t a[4];
+      if constexpr (R == 8) {
+        a[0] = qa[ks][0];
+        a[1] = 0;
+        a[2] = qa[ks][1];
+        a[3] = 0;
+      } else {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[k][e] *= f;
-            } else {
-              o[k][i * 2] *= f;
-              o[k][i * 2 + 1] *= f;
-            }
+        for (int i = 0; i < 4; ++i) a[i] = qa[ks][i];
+      }
+      mma16816<T>(sa[ks & 1][0], a, kf[0], kf[1]);
+      mma16816<T>(sa[ks & 1][1], a, kf[2], kf[3]);
+    }
+    float s[NR][4];                 // keys col, col + 1, col + 8, col + 9
+    float mn[NR];
+    bool grows = false;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      float t = -CUDART_INF_F;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int key = col + (e & 1) + (e >> 1) * 8;
+        const float x = (sa[0][e >> 1][i * 2 + (e & 1)] + sa[1][e >> 1][i * 2 + (e & 1)]) *
+                        p.scale_log2;
+        s[i][e] = (desc.x >> key) & 1 ? x : -CUDART_INF_F;
+        t = fmaxf(t, s[i][e]);
+      }
+      t = fmaxf(t, __shfl_xor_sync(kFull, t, 1));
+      t = fmaxf(t, __shfl_xor_sync(kFull, t, 2));
+      mn[i] = fmaxf(m[i], t);
+      grows |= mn[i] > m[i];
+    }
+    if (__any_sync(kFull, grows)) {
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        const float f = m[i] == mn[i] ? 1.f : sm103::ex2(m[i] - mn[i]);
+        m[i] = mn[i];
+        l[i] *= f;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          if constexpr (R == 8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[k][e] *= f;
+          } else {
+            o[k][i * 2] *= f;
+            o[k][i * 2 + 1] *= f;
           }
         }
       }
-      uint32_t hi[NR][2], lo[NR][2];
-#pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        const float ref = m[i] == -CUDART_INF_F ? 0.f : m[i];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][e] = sm103::ex2(s[i][e] - ref);
-        l[i] += (s[i][0] + s[i][1]) + (s[i][2] + s[i][3]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          hi[i][h] = pack2<T>(s[i][2 * h], s[i][2 * h + 1]);
-          const float2 back = unpack2<T>(hi[i][h]);
-          lo[i][h] = pack2<T>(s[i][2 * h] - back.x, s[i][2 * h + 1] - back.y);
-        }
-      }
-#pragma unroll
-      for (int dt = 0; dt < D / 16; ++dt) {
-        uint32_t vf[4];
-        ldsm4_t(vf, vb + (v_row * CPR + ((dt * 2 + v_ch) ^ swizzle(v_row))) * 16);
-        if constexpr (R == 8) {
-          const uint32_t a[4] = {hi[0][0], lo[0][0], hi[0][1], lo[0][1]};
-          mma16816<T>(o[2 * dt], a, vf[0], vf[1]);
-          mma16816<T>(o[2 * dt + 1], a, vf[2], vf[3]);
-        } else {
-          const uint32_t a[4] = {hi[0][0], hi[1][0], hi[0][1], hi[1][1]};
-          const uint32_t c[4] = {lo[0][0], lo[1][0], lo[0][1], lo[1][1]};
-          mma16816<T>(o[2 * dt], a, vf[0], vf[1]);
-          mma16816<T>(o[2 * dt + 1], a, vf[2], vf[3]);
-          mma16816<T>(o[2 * dt], c, vf[0], vf[1]);
-          mma16816<T>(o[2 * dt + 1], c, vf[2], vf[3]);
-        }
-      }
     }
-
-    __syncthreads();                // the last part's sums have been read
+    uint32_t hi[NR][2], lo[NR][2];
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      if ((lane & 3) == 0) {
-        s_m[warp * R + i * 8 + row] = m[i];
-        s_l[warp * R + i * 8 + row] = l[i];
-      }
-      float *dst = s_o + (warp * R + i * 8 + row) * (D + Sh::PAD) + col;
+      const float ref = m[i] == -CUDART_INF_F ? 0.f : m[i];
 #pragma unroll
-      for (int k = 0; k < D / 8; ++k) {
-        const float2 x = R == 8 ? make_float2(o[k][0] + o[k][2], o[k][1] + o[k][3])
-                                : make_float2(o[k][i * 2], o[k][i * 2 + 1]);
-        *reinterpret_cast<float2 *>(dst + k * 8) = x;
+      for (int e = 0; e < 4; ++e) s[i][e] = sm103::ex2(s[i][e] - ref);
+      l[i] += (s[i][0] + s[i][1]) + (s[i][2] + s[i][3]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        hi[i][h] = pack2<T>(s[i][2 * h], s[i][2 * h + 1]);
+        const float2 back = unpack2<T>(hi[i][h]);
+        lo[i][h] = pack2<T>(s[i][2 * h] - back.x, s[i][2 * h + 1] - back.y);
       }
     }
-    __syncthreads();
-    finish_part<T, D, R, Sh::PAD>(p, part, n0, heads, s_o, s_m, s_l);
-    if (part.first != 0 || part.last != part.blocks) meta.note(part, w.segs);
+#pragma unroll
+    for (int dt = 0; dt < D / 16; ++dt) {
+      uint32_t vf[4];
+      ldsm4_t(vf, vb + (v_row * CPR + ((dt * 2 + v_ch) ^ Sw::at(v_row))) * 16);
+      if constexpr (R == 8) {
+        const uint32_t a[4] = {hi[0][0], lo[0][0], hi[0][1], lo[0][1]};
+        mma16816<T>(o[2 * dt], a, vf[0], vf[1]);
+        mma16816<T>(o[2 * dt + 1], a, vf[2], vf[3]);
+      } else {
+        const uint32_t a[4] = {hi[0][0], hi[1][0], hi[0][1], hi[1][1]};
+        const uint32_t c[4] = {lo[0][0], lo[1][0], lo[0][1], lo[1][1]};
+        mma16816<T>(o[2 * dt], a, vf[0], vf[1]);
+        mma16816<T>(o[2 * dt + 1], a, vf[2], vf[3]);
+        mma16816<T>(o[2 * dt], c, vf[0], vf[1]);
+        mma16816<T>(o[2 * dt + 1], c, vf[2], vf[3]);
+      }
+    }
+
+    if (desc.x & kPartEnds) {
+      const bool ends = desc.x & kSegEnds;
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        l[i] += __shfl_xor_sync(kFull, l[i], 1);
+        l[i] += __shfl_xor_sync(kFull, l[i], 2);
+      }
+      const int id = desc.y * segs + desc.z;
+      if (opens && ends) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const int r = row + i * 8;
+          if (r >= heads) continue;
+          const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+          T *y = static_cast<T *>(p.y) + desc.y * p.y_stride + int64_t(n0 + r) * D + col;
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k) {
+            const float x0 = (R == 8 ? o[k][0] + o[k][2] : o[k][i * 2]) * inv;
+            const float x1 = (R == 8 ? o[k][1] + o[k][3] : o[k][i * 2 + 1]) * inv;
+            if (p.y_pairs) {
+              *reinterpret_cast<uint32_t *>(y + k * 8) = pack2<T>(x0, x1);
+            } else {
+              y[k * 8] = from_f<T>(x0);
+              y[k * 8 + 1] = from_f<T>(x1);
+            }
+          }
+          if ((lane & 3) == 0) write_stats(p, desc.y, n0 + r, m[i] * kLn2, l[i]);
+        }
+      } else {
+        __syncwarp();                // the ring has been read
+        const int slot = opens ? 1 : 0;
+        float *dst = partial_at<NW>(p, R, desc.x & kRangeEnds, my);
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const int r = row + i * 8;
+          if ((lane & 3) == 0) {
+            s_part.m[slot][warp][r] = m[i];
+            s_part.l[slot][warp][r] = l[i];
+          }
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k)
+            *reinterpret_cast<float2 *>(dst + r * (D + Sh::PAD) + col + k * 8) =
+                R == 8 ? make_float2(o[k][0] + o[k][2], o[k][1] + o[k][3])
+                       : make_float2(o[k][i * 2], o[k][i * 2 + 1]);
+        }
+        if (lane == 0) {
+          s_part.id[slot][warp] = id;
+          s_part.ends[slot][warp] = ends;
+          s_part.o[slot][warp] = dst;
+        }
+      }
+    }
   }
-  cp_async_wait<0>();
-  if (tid == 0) meta.store(p);
-  if (err && p.error) atomicOr(p.error, err);
+  __syncthreads();
+  merge_partials<T, D, R, NW, Sh::PAD>(p, chunks, s_part);
+  if (load.err && p.error) atomicOr(p.error, load.err);
 }
 
 // ---------------------------------------------------------------------------
-// CUDA-core kernel.  One warp takes a block of KB keys at a time and holds all
-// R heads' running maximum, sum and output; the warps of a CTA take blocks in
-// turn and meet at the end of a part.
+// fp32 kernel, on the CUDA cores
 // ---------------------------------------------------------------------------
-template <typename T, int D, int R>
-__global__ void __launch_bounds__(kThreads) decode_simt_kernel(const __grid_constant__ DecodeParams p) {
-  constexpr int KB = 8;
-  constexpr int PL = D / 32;      // output dims per lane: lane, lane + 32, ...
-  __shared__ float s_q[R][D];
-  __shared__ __align__(16) float s_o[kWarps][R][D];
-  __shared__ float s_m[kWarps][R], s_l[kWarps][R];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int chunks = (p.group + R - 1) / R;
-  Walk<KB> w;
-  place<KB>(p, p.n_kv * chunks, w);
-  const T *q = static_cast<const T *>(p.q), *kc = static_cast<const T *>(p.kc),
-          *vc = static_cast<const T *>(p.vc);
-  int err = 0;
-  Meta meta;
-  Part part;
-  while (w.next(p, part)) {
-    const Span sp = w.part_span;
-    const int hk = part.seg / chunks, h0 = (part.seg % chunks) * R;
-    const int heads = min(R, p.group - h0);
-    const int n0 = hk * p.group + h0;
-    __syncthreads();
-    for (int i = tid; i < R * D; i += kThreads)
-      s_q[i / D][i % D] =
-          i / D < heads ? to_f(q[part.b * p.q_stride + int64_t(n0 + i / D) * D + i % D]) : 0.f;
-    __syncthreads();
-    float m[R], l[R], o[R][PL];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      m[r] = -CUDART_INF_F;
-      l[r] = 0.f;
-#pragma unroll
-      for (int i = 0; i < PL; ++i) o[r][i] = 0.f;
-    }
-    for (int blk = part.first + warp; blk < part.last; blk += kWarps) {
-      // Lane -> key lane / 4, dims (lane % 4) + 4 i.
-      const int j = (sp.blk0 + blk) * KB + lane / 4;
-      bool ok = j >= sp.lo && j < sp.hi;
-      int64_t off = 0;
-      if (ok) {
-        int tok;
-        const int page = p.table[part.b * p.table_stride + page_of(p, j, tok)];
-        if (page >= 0 && page < p.num_pages) {
-          off = page * p.page_stride + tok * p.token_stride + hk * p.head_stride;
-        } else {
-          ok = false;
-          err = FA_PAGED_BAD_PAGE;
-        }
-      }
-      float s[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) s[r] = 0.f;
-      if (ok) {
-        for (int i = lane & 3; i < D; i += 4) {
-          const float kv = to_f(kc[off + i]);
-#pragma unroll
-          for (int r = 0; r < R; ++r) s[r] = fmaf(s_q[r][i], kv, s[r]);
-        }
-      }
+// Row r's chunk c at chunk c ^ at(r): the eight lanes of a 128-byte shared
+// memory access read two rows' four neighbouring chunks.
+struct SimtSwizzle {
+  static __device__ __forceinline__ int at(int r) { return (r & 1) << 2; }
+};
+
+template <int D, int R>
+using SimtShape = Shape<float, D, R, 8, (R * D + 8 * R) * 4, 2>;
+
+// A warp takes 8 keys at a time.  Scores: four lanes per key, each a quarter
+// of the dims (every fourth chunk).  Output: each lane D / 32 dims of all R heads.
+template <int D, int R>
+__global__ void __launch_bounds__(SimtShape<D, R>::NW * 32, 1)
+decode_simt_kernel(const __grid_constant__ DecodeParams p) {
+  using Sh = SimtShape<D, R>;
+  constexpr int KB = 8, S = Sh::S, NW = Sh::NW;
+  constexpr int CPR = D / 4;
+  constexpr int VW = D % 128 == 0 ? 4 : D % 64 == 0 ? 2 : 1;   // dims per access
+  constexpr int NV = D / (32 * VW);                             // accesses per row
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ Partials<NW, R> s_part;
+  __shared__ int4 s_desc[NW][S];
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float *s_q = reinterpret_cast<float *>(smem + NW * S * Sh::kStage) + warp * (R * D + 8 * R);
+  float *s_p = s_q + R * D;         // q [R][D], weights [8][R]
+  const uint8_t *my = smem + warp * S * Sh::kStage;
+  const uint32_t ring = sm103::smem_u32(my);
+  const int chunks = (p.group + R - 1) / R, segs = p.n_kv * chunks;
+  if (lane < 2) s_part.id[lane][warp] = -1;
+
+  Loader<float, D, KB, S, SimtSwizzle> load(p, blockIdx.x * NW + warp, chunks);
+  load.look();
+#pragma unroll 1
+  for (int i = 0; i < S - 1; ++i) {
+    load.issue(ring + i * Sh::kStage, &s_desc[warp][i]);
+    load.look();
+  }
+
+  const int key = lane >> 2, quarter = lane & 3;
+  int stage = 0, fill = S - 1, heads = 0, n0 = 0;
+  float o[R][NV * VW], m[R], l[R];
+  bool opens = false;
+
+#pragma unroll 1
+  while (true) {
+    cp_async_wait<S - 2>();
+    __syncwarp();
+    const int4 desc = s_desc[warp][stage];
+    if (desc.x & kDone) break;
+    const float *kb = reinterpret_cast<const float *>(my + stage * Sh::kStage);
+    const float *vb = kb + KB * D;
+    load.issue(ring + fill * Sh::kStage, &s_desc[warp][fill]);
+    load.look();
+    fill = fill + 1 == S ? 0 : fill + 1;
+    stage = stage + 1 == S ? 0 : stage + 1;
+
+    if (desc.x & kPartBegins) {
+      const int hk = desc.z / chunks, h0 = (desc.z - hk * chunks) * R;
+      heads = min(R, p.group - h0);
+      n0 = hk * p.group + h0;
+      opens = desc.x & kSegBegins;
+      const float *qr = static_cast<const float *>(p.q) + desc.y * p.q_stride + int64_t(n0) * D;
+      for (int i = lane; i < R * D; i += 32) s_q[i] = i < heads * D ? __ldg(qr + i) : 0.f;
+      __syncwarp();
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
-        s[r] += __shfl_xor_sync(0xffffffffu, s[r], 2);
-        s[r] = ok ? s[r] * p.scale_log2 : -CUDART_INF_F;
-        float t = s[r];
+        m[r] = -CUDART_INF_F;
+        l[r] = 0.f;
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
-        const float mn = fmaxf(m[r], t), ref = mn == -CUDART_INF_F ? 0.f : mn;
-        const float a = exp2f(m[r] - ref);
-        m[r] = mn;
-        s[r] = exp2f(s[r] - ref);
-        t = s[r];
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
-        l[r] = l[r] * a + t;
-#pragma unroll
-        for (int i = 0; i < PL; ++i) o[r][i] *= a;
-      }
-#pragma unroll
-      for (int k = 0; k < KB; ++k) {
-        const int64_t off_k = __shfl_sync(0xffffffffu, off, 4 * k);
-        if (!__shfl_sync(0xffffffffu, int(ok), 4 * k)) continue;
-        float pk[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) pk[r] = __shfl_sync(0xffffffffu, s[r], 4 * k);
-#pragma unroll
-        for (int i = 0; i < PL; ++i) {
-          const float vv = to_f(vc[off_k + lane + 32 * i]);
-#pragma unroll
-          for (int r = 0; r < R; ++r) o[r][i] = fmaf(pk[r], vv, o[r][i]);
-        }
+        for (int i = 0; i < NV * VW; ++i) o[r][i] = 0.f;
       }
     }
+
+    float s[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) s[r] = 0.f;
+#pragma unroll
+    for (int i = 0; i < CPR / 4; ++i) {
+      const int c = i * 4 + quarter;
+      const float4 kv =
+          *reinterpret_cast<const float4 *>(kb + (key * CPR + (c ^ SimtSwizzle::at(key))) * 4);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float4 qv = *reinterpret_cast<const float4 *>(s_q + r * D + c * 4);
+        s[r] = fmaf(kv.x, qv.x, s[r]);
+        s[r] = fmaf(kv.y, qv.y, s[r]);
+        s[r] = fmaf(kv.z, qv.z, s[r]);
+        s[r] = fmaf(kv.w, qv.w, s[r]);
+      }
+    }
+    const bool ok = (desc.x >> key) & 1;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (lane == 0) {
-        s_m[warp][r] = m[r];
-        s_l[warp][r] = l[r];
-      }
+      s[r] += __shfl_xor_sync(kFull, s[r], 1);
+      s[r] += __shfl_xor_sync(kFull, s[r], 2);
+      s[r] = ok ? s[r] * p.scale_log2 : -CUDART_INF_F;
+      float t = s[r];
 #pragma unroll
-      for (int i = 0; i < PL; ++i) s_o[warp][r][lane + 32 * i] = o[r][i];
+      for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, x));
+      const float mn = fmaxf(m[r], t);
+      if (mn > m[r]) {               // the same for the whole warp
+        const float f = exp2f(m[r] - mn);
+        m[r] = mn;
+        l[r] *= f;
+#pragma unroll
+        for (int i = 0; i < NV * VW; ++i) o[r][i] *= f;
+      }
+      s[r] = exp2f(s[r] - (m[r] == -CUDART_INF_F ? 0.f : m[r]));
+      l[r] += s[r];                  // each key's weight in its four lanes
     }
-    __syncthreads();
-    finish_part<T, D, R, 0>(p, part, n0, heads, &s_o[0][0][0], &s_m[0][0], &s_l[0][0]);
-    if (part.first != 0 || part.last != part.blocks) meta.note(part, w.segs);
+    if (quarter == 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) s_p[key * R + r] = s[r];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+      float pk[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) pk[r] = s_p[k * R + r];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int d = (i * 32 + lane) * VW;
+        const float *src = vb + (k * CPR + ((d >> 2) ^ SimtSwizzle::at(k))) * 4 + (d & 3);
+        float v[VW];
+        if constexpr (VW == 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(src);
+          v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+        } else if constexpr (VW == 2) {
+          const float2 x = *reinterpret_cast<const float2 *>(src);
+          v[0] = x.x; v[1] = x.y;
+        } else {
+          v[0] = *src;
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int e = 0; e < VW; ++e) o[r][i * VW + e] = fmaf(pk[r], v[e], o[r][i * VW + e]);
+      }
+    }
+
+    if (desc.x & kPartEnds) {
+      const bool ends = desc.x & kSegEnds;
+      const int id = desc.y * segs + desc.z;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[r] += __shfl_xor_sync(kFull, l[r], x);
+      }
+      const bool whole = opens && ends;
+      const int slot = opens ? 1 : 0;
+      float *dst = partial_at<NW>(p, R, desc.x & kRangeEnds, my);
+      __syncwarp();                  // the ring has been read
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r >= heads) continue;
+        const float inv = whole ? (l[r] == 0.f ? 0.f : 1.f / l[r]) : 1.f;
+        float *to = whole ? static_cast<float *>(p.y) + desc.y * p.y_stride + int64_t(n0 + r) * D
+                          : dst + r * (D + Sh::PAD);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int e = 0; e < VW; ++e) to[(i * 32 + lane) * VW + e] = o[r][i * VW + e] * inv;
+        if (lane == 0) {
+          if (whole) {
+            write_stats(p, desc.y, n0 + r, m[r] * kLn2, l[r]);
+          } else {
+            s_part.m[slot][warp][r] = m[r];
+            s_part.l[slot][warp][r] = l[r];
+          }
+        }
+      }
+      if (lane == 0 && !whole) {
+        s_part.id[slot][warp] = id;
+        s_part.ends[slot][warp] = ends;
+        s_part.o[slot][warp] = dst;
+      }
+    }
   }
-  if (tid == 0) meta.store(p);
-  if (err && p.error) atomicOr(p.error, err);
+  __syncthreads();
+  merge_partials<float, D, R, NW, Sh::PAD>(p, chunks, s_part);
+  if (load.err && p.error) atomicOr(p.error, load.err);
 }
 
 // ---------------------------------------------------------------------------
-// Joins the parts of the segments that were cut: block (i, r) takes query head
-// r of the segment that CTA i began.  Its warps take the parts in turn, so
-// that their loads overlap, and meet in shared memory, always in the same
-// order.
+// Joins the sums of the segments that were cut between CTAs.  Block (x, r)
+// takes query head r of segment x, or, where there are more segments than
+// CTAs, of the segment in which CTA x's ranges end.  Which CTAs share it
+// follows from the lengths alone, so all that is worked out before the main
+// kernel is done.  The warps take the parts in turn, so that their loads
+// overlap, and meet in shared memory, always in the same order.
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
 
-template <typename T, int D>
+template <typename T, int D, int KB, int NW>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(
-    const __grid_constant__ DecodeParams p, int rows) {
+    const __grid_constant__ DecodeParams p, int rows, int by_segment) {
   constexpr int PL = D / 32;
+  constexpr int U = 2;               // parts on the way at once, per warp
   __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
   __shared__ float s_o[kJoinWarps][D];
-  // Launched while the main kernel may still run: nothing of it is read before.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int i = blockIdx.x, r = blockIdx.y;
-  const int id = p.meta[i * 4 + 2];
-  if (id < 0) return;
-  const int chunks = (p.group + rows - 1) / rows;
-  const int segs = p.n_kv * chunks;
-  const int b = id / segs, seg = id % segs;
-  const int h = (seg % chunks) * rows + r;
-  if (h >= p.group) return;
-  const int n = (seg / chunks) * p.group + h;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // Part 0 is CTA i's slot 1, part k CTA (i + k)'s slot 0.
-  int parts = 1;
-  for (bool more = true; more; ) {
-    const int j = i + parts + lane;
-    const bool mine = j < p.grid && p.meta[j * 4] == id;
-    const uint32_t got = __ballot_sync(0xffffffffu, mine);
-    const int run = got == 0xffffffffu ? 32 : __ffs(~got) - 1;
-    parts += run;
-    more = run == 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y;
+  const int chunks = (p.group + rows - 1) / rows, segs = p.n_kv * chunks;
+  Line line;
+  Place at;
+  int first_unit;                    // of the segment
+  if (by_segment) {
+    at.b = blockIdx.x / segs;
+    at.seg = blockIdx.x - at.b * segs;
+    first_unit = segment_start<KB>(p, segs, at, line);
+  } else {
+    const int behind = (blockIdx.x + 1) * NW;
+    find<KB>(p, segs, behind, 1, line, at);
+    first_unit = line.start(behind) - 1 - at.off;
   }
+  // The CTAs of its first and last block.
+  const int i = line.range_of(first_unit + (kSwitchBlocks >> p.unit_shift)) / NW;
+  const int last = line.range_of(first_unit + at.units - 1) / NW;
+  const int h = (chunks == 1 ? 0 : at.seg % chunks * rows) + r;
+  const int n = (chunks == 1 ? at.seg : at.seg / chunks) * p.group + h;
+
+  // Every block waits, also one with nothing to do: what follows on the stream
+  // is behind the main kernel only through this one.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (i == last || h >= p.group || (!by_segment && i != int(blockIdx.x))) return;
+  // Part 0 is CTA i's slot 1, part k CTA (i + k)'s slot 0.
+  const int parts = last - i + 1;
   float mx = -CUDART_INF_F, sum = 0.f, acc[PL];
 #pragma unroll
   for (int k = 0; k < PL; ++k) acc[k] = 0.f;
-#pragma unroll 2
-  for (int j = warp; j < parts; j += kJoinWarps) {
-    const float *src = slot_of(p, i + j, j == 0 ? 1 : 0, rows);
-    const float m2 = src[rows * D + r], l2 = src[rows * D + rows + r];
-    const float mn = fmaxf(mx, m2), ref = mn == -CUDART_INF_F ? 0.f : mn;
-    const float f = exp2f(mx - ref), f2 = exp2f(m2 - ref);
-    mx = mn;
-    sum = sum * f + l2 * f2;
+#pragma unroll 1
+  for (int j0 = warp; j0 < parts; j0 += U * kJoinWarps) {
+    float m2[U], l2[U], o2[U][PL];
 #pragma unroll
-    for (int k = 0; k < PL; ++k) acc[k] = acc[k] * f + src[r * D + lane + 32 * k] * f2;
+    for (int u = 0; u < U; ++u) {
+      const int j = min(j0 + u * kJoinWarps, parts - 1);
+      const float *src = slot_of(p, i + j, j == 0 ? 1 : 0, rows);
+      m2[u] = src[rows * D + r];
+      l2[u] = src[rows * D + rows + r];
+#pragma unroll
+      for (int k = 0; k < PL; ++k) o2[u][k] = src[r * D + lane + 32 * k];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (j0 + u * kJoinWarps >= parts) break;
+      const float mn = fmaxf(mx, m2[u]), ref = mn == -CUDART_INF_F ? 0.f : mn;
+      const float f = sm103::ex2(mx - ref), f2 = sm103::ex2(m2[u] - ref);
+      mx = mn;
+      sum = sum * f + l2[u] * f2;
+#pragma unroll
+      for (int k = 0; k < PL; ++k) acc[k] = acc[k] * f + o2[u][k] * f2;
+    }
   }
   if (lane == 0) {
     s_m[warp] = mx;
@@ -746,24 +1004,36 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(
 #pragma unroll
   for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, s_m[k]);
   const float ref = top == -CUDART_INF_F ? 0.f : top;
-  float total = 0.f, o = 0.f;
+  float total = 0.f, out = 0.f;
 #pragma unroll
   for (int k = 0; k < kJoinWarps; ++k) {
-    const float f = exp2f(s_m[k] - ref);
+    const float f = sm103::ex2(s_m[k] - ref);
     total += f * s_l[k];
-    o += f * s_o[k][d];
+    out += f * s_o[k][d];
   }
-  static_cast<T *>(p.y)[b * p.y_stride + int64_t(n) * D + d] =
-      from_f<T>(total == 0.f ? 0.f : o / total);
-  if (d == 0) write_stats(p, b, n, top * kLn2, total);
+  static_cast<T *>(p.y)[at.b * p.y_stride + int64_t(n) * D + d] =
+      from_f<T>(total == 0.f ? 0.f : out / total);
+  if (d == 0) write_stats(p, at.b, n, top * kLn2, total);
 }
 
-// The join is launched as a dependent of the main kernel, so that its launch
-// overlaps the main kernel's run.
-template <typename T, int D>
-cudaError_t launch_join(const DecodeParams &p, int rows, cudaStream_t s) {
+// The main kernel and the join, which is launched as its dependent so that its
+// launch overlaps the main kernel's run.
+template <typename T, int D, int R, int KB, int NW, typename Kernel>
+cudaError_t launch_both(DecodeParams p, Kernel kernel, int smem, int sms, cudaStream_t s) {
+  p.grid = sms;
+  p.ranges = sms * NW;
+  const int64_t segments = int64_t(p.batch) * p.n_kv * ((p.group + R - 1) / R);
+  const int64_t blocks = (int64_t(p.max_pages) * p.page_size + KB - 1) / KB + 1 + kSwitchBlocks;
+  p.unit_shift = 0;
+  while (segments * ((blocks >> p.unit_shift) + 1) >= (int64_t(1) << 31)) ++p.unit_shift;
+  cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<p.grid, NW * 32, smem, s>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int by_segment = segments <= p.grid;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.grid, rows);
+  cfg.gridDim = dim3(unsigned(by_segment ? segments : p.grid), unsigned(p.group < R ? p.group : R));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr{};
@@ -771,28 +1041,19 @@ cudaError_t launch_join(const DecodeParams &p, int rows, cudaStream_t s) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<T, D>, p, rows);
+  return cudaLaunchKernelEx(&cfg, join_kernel<T, D, KB, NW>, p, R, by_segment);
 }
 
 template <int D, int R>
-cudaError_t launch_simt(DecodeParams p, int sms, cudaStream_t s) {
-  p.grid = sms * kDecodeCtasPerSm;
-  decode_simt_kernel<float, D, R><<<p.grid, kThreads, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_join<float, D>(p, R, s);
+cudaError_t launch_simt(const DecodeParams &p, int sms, cudaStream_t s) {
+  using Sh = SimtShape<D, R>;
+  return launch_both<float, D, R, 8, Sh::NW>(p, decode_simt_kernel<D, R>, Sh::kSmem, sms, s);
 }
 
 template <typename T, int D, int R>
-cudaError_t launch_tc(DecodeParams p, int sms, cudaStream_t s) {
+cudaError_t launch_tc(const DecodeParams &p, int sms, cudaStream_t s) {
   using Sh = TcShape<D, R>;
-  static_assert(Sh::kCtas <= kDecodeCtasPerSm, "workspace size");
-  p.grid = sms * Sh::kCtas;
-  const cudaError_t e = cudaFuncSetAttribute(
-      decode_tc_kernel<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
-  if (e != cudaSuccess) return e;
-  decode_tc_kernel<T, D, R><<<p.grid, kThreads, Sh::kSmem, s>>>(p);
-  const cudaError_t e2 = cudaGetLastError();
-  return e2 != cudaSuccess ? e2 : launch_join<T, D>(p, R, s);
+  return launch_both<T, D, R, 16, Sh::NW>(p, decode_tc_kernel<T, D, R>, Sh::kSmem, sms, s);
 }
 
 template <int D>
@@ -813,9 +1074,9 @@ cudaError_t launch_d(const DecodeParams &p, fa_dtype dt, int rows, int sms, cuda
 
 }  // namespace
 
-// fp32: the heads that a lane's registers hold at once.  16-bit types: the
-// rows of one product, all 16 of which serve P rounded once a group has more
-// than 8 heads.
+// fp32: the heads whose outputs a lane's registers hold at once.  16-bit types:
+// the rows of one product, all 16 of which serve P rounded once a group has
+// more than 8 heads.
 int decode_rows(fa_dtype dt, int group) {
   if (dt != FA_DTYPE_FP32) return group <= 8 ? 8 : 16;
   return group <= 1 ? 1 : group <= 2 ? 2 : group <= 4 ? 4 : 8;
