@@ -417,8 +417,7 @@ def _elsewhere(index, stream):
     return stream is not None or torch._C._cuda_getDevice() != index
 
 
-def _raw_stream(index):
-    return torch._C._cuda_getCurrentRawStream(index)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _refuse(name, t, expected, index=None):
@@ -437,8 +436,8 @@ def _device_of(t, name):
 
 def _flat(t, dtype, count, index, name):
     """A contiguous one-dimensional tensor of `count` entries."""
-    if not (t.get_device() == index and t.dtype is dtype and t.dim() == 1 and
-            t.numel() == count and t.is_contiguous()):
+    if not (t.get_device() == index and t.dtype is dtype and t.shape == (count,) and
+            t.is_contiguous()):
         _refuse(name, t, f"contiguous {dtype} [{count}]", index)
     return t.data_ptr()
 
@@ -488,29 +487,39 @@ def paged_plan(block_table, seq_lens, delta, free_pages, free_state, page_size, 
         with _On(index, stream):
             return paged_plan(block_table, seq_lens, delta, free_pages, free_state, page_size,
                               max_tokens, slots, cu_tokens, seq_lens_out, free_state_out, error)
+    i32, i64, empty = torch.int32, torch.int64, torch.empty
     max_pages, stride = _table(block_table, index)
-    b, pages, max_tokens = block_table.shape[0], free_pages.numel(), int(max_tokens)
+    b, pages, max_tokens = block_table.size(0), free_pages.numel(), int(max_tokens)
     dev = block_table.device
     if slots is None:
-        slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+        slots = empty(max_tokens, dtype=i64, device=dev)
+        at_slots = slots.data_ptr()
+    else:
+        at_slots = _flat(slots, i64, max_tokens, index, "slots")
     if cu_tokens is None:
-        cu_tokens = torch.empty(b + 1, dtype=torch.int64, device=dev)
+        cu_tokens = empty(b + 1, dtype=i64, device=dev)
+        at_cu = cu_tokens.data_ptr()
+    else:
+        at_cu = _flat(cu_tokens, i64, b + 1, index, "cu_tokens")
     if seq_lens_out is None:
-        seq_lens_out = torch.empty(b, dtype=torch.int32, device=dev)
+        seq_lens_out = empty(b, dtype=i32, device=dev)
+        at_lens = seq_lens_out.data_ptr()
+    else:
+        at_lens = _flat(seq_lens_out, i32, b, index, "seq_lens_out")
     if free_state_out is None:
-        free_state_out = torch.empty(2, dtype=torch.int64, device=dev)
-    i32, i64 = torch.int32, torch.int64
-    _check(lib().fa_paged_plan(
+        free_state_out = empty(2, dtype=i64, device=dev)
+        at_state = free_state_out.data_ptr()
+    else:
+        at_state = _flat(free_state_out, i64, 2, index, "free_state_out")
+    status = (_LIB or lib()).fa_paged_plan(
         block_table.data_ptr(), max_pages, stride, _flat(seq_lens, i32, b, index, "seq_lens"),
         _flat(delta, i32, b, index, "delta"), b,
         _flat(free_pages, i32, pages, index, "free_pages"),
-        _flat(free_state, i64, 2, index, "free_state"), pages, int(page_size),
-        _flat(slots, i64, max_tokens, index, "slots"), max_tokens,
-        _flat(cu_tokens, i64, b + 1, index, "cu_tokens"),
-        _flat(seq_lens_out, i32, b, index, "seq_lens_out"),
-        _flat(free_state_out, i64, 2, index, "free_state_out"),
-        None if error is None else _flat(error, i32, 1, index, "error"), _raw_stream(index)),
-        "fa_paged_plan")
+        _flat(free_state, i64, 2, index, "free_state"), pages, int(page_size), at_slots,
+        max_tokens, at_cu, at_lens, at_state,
+        None if error is None else _flat(error, i32, 1, index, "error"), _raw_stream(index))
+    if status:
+        _check(status, "fa_paged_plan")
     return slots, cu_tokens, seq_lens_out, free_state_out
 
 
@@ -524,13 +533,15 @@ def paged_write(k, v, slots, k_pages, v_pages, error=None, stream=None):
             return paged_write(k, v, slots, k_pages, v_pages, error)
     shape, strides = _pages(k_pages, v_pages, index)
     tokens, dtype = slots.numel(), k_pages.dtype
-    _check(lib().fa_paged_write(
+    status = (_LIB or lib()).fa_paged_write(
         k.data_ptr(), v.data_ptr(), _rows(k, tokens, shape[2], shape[3], dtype, index, "k"),
         _rows(v, tokens, shape[2], shape[3], dtype, index, "v"),
         _flat(slots, torch.int64, tokens, index, "slots"), tokens, k_pages.data_ptr(),
         v_pages.data_ptr(), *shape, strides[0], strides[1], strides[2], _DTYPE[dtype],
         None if error is None else _flat(error, torch.int32, 1, index, "error"),
-        _raw_stream(index)), "fa_paged_write")
+        _raw_stream(index))
+    if status:
+        _check(status, "fa_paged_write")
 
 
 def paged_decode_workspace_size(batch, n, n_kv, d, dtype) -> int:
@@ -562,12 +573,11 @@ def paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, pre_tokens=2
                                 stats, softmax_max, softmax_sum, workspace, error)
     shape, strides = _pages(k_pages, v_pages, index)
     max_pages, table_stride = _table(block_table, index)
-    if q.dim() != 3:
+    b, heads, (_, _, n_kv, d) = block_table.size(0), q.shape, shape
+    if len(heads) != 3:
         _refuse("q", q, "[batch, heads, dim]", index)
-    b, n, n_kv, d = block_table.shape[0], q.shape[1], shape[2], shape[3]
-    dtype = k_pages.dtype
+    n, dtype, dev = heads[1], k_pages.dtype, k_pages.device
     qs = _rows(q, b, n, d, dtype, index, "q")
-    dev = k_pages.device
     if y is None:
         y, ys = torch.empty((b, n, d), dtype=dtype, device=dev), n * d
     else:
@@ -590,11 +600,13 @@ def paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, pre_tokens=2
         nbytes = workspace.numel() * workspace.element_size()
         if not (workspace.is_contiguous() and workspace.get_device() == index):
             _refuse("workspace", workspace, "contiguous memory", index)
-    _check(lib().fa_paged_decode(
+    status = (_LIB or lib()).fa_paged_decode(
         q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), shape[0], shape[1], strides[0],
         strides[1], strides[2], block_table.data_ptr(), max_pages, table_stride,
         _flat(seq_lens, torch.int32, b, index, "seq_lens"), b, n, n_kv, d, _DTYPE[dtype], scale,
         min(max(int(pre_tokens), -1), 2 ** 40), y.data_ptr(), ys, top, total,
         None if error is None else _flat(error, torch.int32, 1, index, "error"),
-        workspace.data_ptr(), nbytes, _raw_stream(index)), "fa_paged_decode")
+        workspace.data_ptr(), nbytes, _raw_stream(index))
+    if status:
+        _check(status, "fa_paged_decode")
     return y, softmax_max, softmax_sum

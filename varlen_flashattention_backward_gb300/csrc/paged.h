@@ -20,7 +20,8 @@ struct PlanParams {
   int64_t *state_out;
   int32_t *error;
   int64_t max_tokens;
-  int batch, max_pages, num_pages, page_size;
+  int batch, max_pages, num_pages, page_size, page_shift;   // page_shift: log2 or -1
+  int phases;   // set at launch
 };
 
 struct WriteParams {
@@ -31,7 +32,7 @@ struct WriteParams {
   int64_t n_slots;
   int64_t page_stride, token_stride, head_stride;
   int32_t *error;
-  int tokens, page_size, n_kv, d;
+  int tokens, page_size, page_shift, n_kv, d;
 };
 
 struct DecodeParams {

@@ -90,6 +90,14 @@ bool element_aligned(const void *ptr, fa_dtype dt) {
   return reinterpret_cast<uintptr_t>(ptr) % (dt == FA_DTYPE_FP32 ? 4 : 2) == 0;
 }
 
+// log2 of a power of 2, -1 for another number.
+int log2_or_none(int64_t x) {
+  if ((x & (x - 1)) != 0) return -1;
+  int n = 0;
+  while ((int64_t(1) << n) < x) ++n;
+  return n;
+}
+
 struct DecodeLayout {
   size_t part, warp_part, total;
 };
@@ -139,6 +147,7 @@ fa_status fa_paged_plan(int32_t *block_table, int64_t max_pages, int64_t table_s
   p.max_pages = int(max_pages);
   p.num_pages = int(num_pages);
   p.page_size = int(page_size);
+  p.page_shift = log2_or_none(page_size);
   return launch_paged_plan(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
                                                                                      : FA_ERR_CUDA;
 }
@@ -177,6 +186,7 @@ fa_status fa_paged_write(const void *k, const void *v, int64_t k_stride, int64_t
   p.error = error;
   p.tokens = int(tokens);
   p.page_size = int(page_size);
+  p.page_shift = log2_or_none(page_size);
   p.n_kv = int(head_num_kv);
   p.d = int(head_dim);
   return launch_paged_write(p, dtype, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
@@ -245,11 +255,7 @@ fa_status fa_paged_decode(const void *q, int64_t q_stride, const void *k_pages,
   p.warp_part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.warp_part);
   p.num_pages = int(num_pages);
   p.page_size = int(page_size);
-  p.page_shift = -1;
-  if ((page_size & (page_size - 1)) == 0) {
-    p.page_shift = 0;
-    while ((int64_t(1) << p.page_shift) < page_size) ++p.page_shift;
-  }
+  p.page_shift = log2_or_none(page_size);
   p.max_pages = int(max_pages);
   p.batch = int(batch);
   p.n = int(head_num);

@@ -5,201 +5,261 @@
 namespace fav {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kPerThread = 2;   // requests per thread: kThreads * kPerThread = the largest batch
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxPer = 4;                        // requests per thread
+constexpr int kMaxRequests = kThreads * kMaxPer;  // the largest batch
 
-struct Sums {
-  int64_t rows, need, give;
-};
-
-// What one request asks for, from its length and delta alone.
-struct Ask {
-  int64_t rows;      // packed rows
-  int have, target;  // pages held, length wanted
-  bool sound, grow, in_row;
-};
-
-__device__ __forceinline__ int pages_of(int64_t len, int page_size) {
-  return int((len + page_size - 1) / page_size);
-}
-
-__device__ __forceinline__ Ask ask_of(const PlanParams &p, int len, int delta) {
-  Ask a;
-  const int64_t most = int64_t(p.max_pages) * p.page_size;
-  a.rows = delta > 0 ? delta : 0;
-  a.sound = len >= 0 && len <= most;
-  a.grow = a.sound && delta > 0;
-  int64_t target = int64_t(len) + delta;
-  if (target < 0) target = 0;
-  a.in_row = target <= most;
-  a.target = int(a.in_row ? target : 0);
-  a.have = a.sound ? pages_of(len, p.page_size) : 0;
-  return a;
-}
-
-// Exclusive block-wide prefix of v over the threads; `total` gets the sum.
-__device__ int64_t block_prefix(int64_t v, int64_t *buf, int64_t &total) {
+// Exclusive prefix of v over the CTA's threads; `total` gets the sum.  `buf`
+// holds kWarps values and is not written again before the next barrier.
+__device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t *buf, int64_t &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    const int64_t y = __shfl_up_sync(kFull, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) buf[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int64_t w = buf[lane];
+  int64_t before = x - v;
+  total = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    buf[lane] = w;
+  for (int i = 0; i < kWarps; ++i) {
+    const int64_t w = buf[i];
+    if (i < warp) before += w;
+    total += w;
   }
-  __syncthreads();
-  total = buf[31];
-  const int64_t before = (warp ? buf[warp - 1] : 0) + x - v;
-  __syncthreads();
   return before;
 }
 
-__device__ __forceinline__ int ring_at(const PlanParams &p, int64_t i) {
-  return int(i >= p.num_pages ? i - p.num_pages : i);
+// What the flat loops read of each request.
+struct Requests {
+  int row[kMaxRequests + 1];   // first packed row
+  int need[kMaxRequests];      // pages taken before it (up to the last granted)
+  int give[kMaxRequests + 1];  // pages given back before it
+  int len[kMaxRequests];
+  int have[kMaxRequests];      // pages held
+  uint8_t granted[kMaxRequests];
+};
+
+// The request with first[b] <= i < first[b + 1].
+__device__ __forceinline__ int owner_of(const int *first, int n, int i) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= i) lo = mid; else hi = mid - 1;
+  }
+  return lo;
 }
 
-// One CTA.  Phase 1: three block-wide prefix sums over the requests (rows,
-// pages taken, pages given).  Phase 2: pages and slots, flat over all of
-// them.  Phase 3: lengths and pool, which may be the inputs.
-__global__ void __launch_bounds__(kThreads) plan_kernel(PlanParams p) {
-  __shared__ int64_t buf[32];
-  __shared__ int64_t s_row[kThreads * kPerThread + 1];   // first packed row of each request
-  __shared__ int s_off[kThreads * kPerThread];           // first page taken or given
-  __shared__ int s_len[kThreads * kPerThread];
-  __shared__ uint8_t s_kind[kThreads * kPerThread];      // 1: granted, 2: shrinks
+__device__ __forceinline__ int wrap(int64_t i, int n) { return int(i >= n ? i - n : i); }
+
+// Phase 1: prefix sums over the requests, of rows, then of pages taken and
+// given back.  Phase 2, over the packed rows and the moved pages, a warp
+// taking a run of them: one binary search at its start, then a walk.  The
+// pages that a request takes are read from the ring, not from the table, so
+// that nothing in phase 2 depends on anything else in it.  Phase 3: lengths
+// and pool, which may be updated in place.
+//
+// A small call is one CTA that does all three.  A large one spreads phase 2
+// over many CTAs, each of which does phase 1 for itself, and leaves phase 3 to
+// one more CTA, launched as their dependent: it does its phase 1 beside them
+// and writes when they are done.
+enum : int { kFill = 1, kCommit = 2 };
+
+__global__ void __launch_bounds__(kThreads, 1) plan_kernel(const __grid_constant__ PlanParams p) {
+  __shared__ int64_t buf[3][kWarps];
+  __shared__ Requests s;
+  __shared__ int s_taken;
+  asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x;
+  const bool first_cta = (p.phases & kFill) && blockIdx.x == 0;
+  const int per = (p.batch + kThreads - 1) / kThreads;
+  const int64_t most = int64_t(p.max_pages) * p.page_size;
+  if (tid == 0) s_taken = 0;
   int err = 0;
 
-  int len[kPerThread], delta[kPerThread];
-  Ask a[kPerThread];
+  int len[kMaxPer], delta[kMaxPer];
+  const int64_t head = p.state[0], count = p.state[1];
   int64_t rows = 0;
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = tid * kPerThread + i;
-    len[i] = b < p.batch ? p.lens[b] : 0;
-    delta[i] = b < p.batch ? p.delta[b] : 0;
-    a[i] = ask_of(p, len[i], delta[i]);
-    rows += a[i].rows;
-    if (!a[i].sound) err |= FA_PAGED_BAD_LENGTH;
-    if (a[i].grow && !a[i].in_row) err |= FA_PAGED_ROW_FULL;
+  for (int i = 0; i < kMaxPer; ++i) {
+    const int b = tid * per + i;
+    const bool in = i < per && b < p.batch;
+    len[i] = in ? p.lens[b] : 0;
+    delta[i] = in ? p.delta[b] : 0;
+    rows += max(delta[i], 0);
   }
-  const int64_t head = p.state[0], count = p.state[1];
   int64_t total_rows, total_need, total_give;
-  int64_t row = block_prefix(rows, buf, total_rows);
+  int64_t row = block_prefix(rows, buf[0], total_rows);
 
-  int need[kPerThread], give[kPerThread];
-  bool ask[kPerThread];
-  int64_t needs = 0, gives = 0;
+  int need[kMaxPer], give[kMaxPer], target[kMaxPer], have[kMaxPer];
+  bool ask[kMaxPer];
+  int64_t first_row[kMaxPer], needs = 0, gives = 0;
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = tid * kPerThread + i;
-    s_row[b] = row;
-    row += a[i].rows;
-    ask[i] = a[i].grow && a[i].in_row && row <= p.max_tokens;
-    if (a[i].grow && a[i].in_row && !ask[i]) err |= FA_PAGED_ROWS;
-    const int want = pages_of(a[i].target, p.page_size);
-    need[i] = ask[i] ? want - a[i].have : 0;
-    give[i] = a[i].sound && delta[i] < 0 ? a[i].have - want : 0;
+  for (int i = 0; i < kMaxPer; ++i) {
+    const bool sound = len[i] >= 0 && len[i] <= most;
+    const int64_t want_len = max(int64_t(len[i]) + delta[i], int64_t(0));
+    const bool in_row = want_len <= most;
+    first_row[i] = row;
+    row += max(delta[i], 0);
+    const bool grows = sound && delta[i] > 0 && in_row;
+    ask[i] = grows && row <= p.max_tokens;
+    if (!sound) err |= FA_PAGED_BAD_LENGTH;
+    if (sound && delta[i] > 0 && !in_row) err |= FA_PAGED_ROW_FULL;
+    if (grows && !ask[i]) err |= FA_PAGED_ROWS;
+    have[i] = sound ? (len[i] + p.page_size - 1) / p.page_size : 0;
+    target[i] = in_row ? int(want_len) : 0;
+    const int want = (target[i] + p.page_size - 1) / p.page_size;
+    need[i] = ask[i] ? want - have[i] : 0;
+    give[i] = sound && delta[i] < 0 ? have[i] - want : 0;
     needs += need[i];
     gives += give[i];
   }
-  if (tid == kThreads - 1) s_row[kThreads * kPerThread] = row;
-  int64_t off_need = block_prefix(needs, buf, total_need);
-  int64_t off_give = block_prefix(gives, buf, total_give);
-  // Granted requests are a prefix of those that need pages, so their pages
-  // start where the sum over all before them says.
-  int64_t granted_pages = 0;
-  bool granted[kPerThread];
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = tid * kPerThread + i;
-    granted[i] = ask[i] && (need[i] == 0 || off_need + need[i] <= count);
-    if (ask[i] && !granted[i]) err |= FA_PAGED_EXHAUSTED;
-    if (granted[i]) granted_pages += need[i];
-    s_off[b] = int(granted[i] ? off_need : off_give);
-    s_len[b] = len[i];
-    s_kind[b] = granted[i] ? 1 : (a[i].sound && delta[i] < 0) ? 2 : 0;
-    off_need += need[i];
-    off_give += give[i];
-  }
-  int64_t taken;
-  block_prefix(granted_pages, buf, taken);
+  int64_t off_need = block_prefix(needs, buf[1], total_need);
+  int64_t off_give = block_prefix(gives, buf[2], total_give);
   // With room for all of them behind the end, the pages given back land on no
   // entry that this call takes.
   const bool whole = head >= 0 && head < p.num_pages && count >= 0 && count <= p.num_pages &&
                      count + total_give <= p.num_pages;
   if (!whole) err |= FA_PAGED_BAD_POOL;
-  // Row starts of requests behind the batch equal the total, which s_row[batch]
-  // then holds.
-  for (int b = tid; b <= p.batch; b += kThreads) p.cu[b] = s_row[b];
-
-  if (whole) {
-    const int warp = tid >> 5, lane = tid & 31;
-    for (int b = warp; b < p.batch; b += kThreads / 32) {
-      const int kind = s_kind[b];
-      if (kind == 0) continue;
-      const int64_t d = p.delta[b], l = s_len[b];
-      const int64_t target = l + d < 0 ? 0 : l + d;
-      const int have = pages_of(l, p.page_size), want = pages_of(target, p.page_size);
-      int32_t *tab = p.table + b * p.table_stride;
-      if (kind == 1) {
-        for (int i = lane; i < want - have; i += 32)
-          tab[have + i] = p.ring[ring_at(p, head + s_off[b] + i)];
-      } else {
-        const int64_t base = (head + count) % p.num_pages;
-        for (int i = lane; i < have - want; i += 32)
-          p.ring[ring_at(p, base + s_off[b] + i)] = tab[want + i];
-      }
+  bool granted[kMaxPer];
+  int64_t granted_upto = 0;
+#pragma unroll
+  for (int i = 0; i < kMaxPer; ++i) {
+    const int b = tid * per + i;
+    const bool in = i < per && b < p.batch;
+    // Of the requests that need pages a prefix is granted, so the sum over all
+    // before a granted one is the sum over the granted ones.
+    granted[i] = ask[i] && (need[i] == 0 || off_need + need[i] <= count);
+    if (ask[i] && !granted[i]) err |= FA_PAGED_EXHAUSTED;
+    if (granted[i] && need[i] > 0) granted_upto = off_need + need[i];
+    if (in) {
+      s.row[b] = int(min(first_row[i], p.max_tokens));
+      s.need[b] = int(min(off_need, max(count, int64_t(0))));
+      s.give[b] = int(min(off_give, int64_t(p.num_pages)));
+      s.len[b] = len[i];
+      s.have[b] = have[i];
+      s.granted[b] = granted[i] && whole;
+      if (first_cta) p.cu[b] = first_row[i];
     }
+    off_need += need[i];
+    off_give += give[i];
+  }
+  if (granted_upto > 0) atomicMax(&s_taken, int(granted_upto));
+  if (tid == 0) {
+    s.row[p.batch] = int(min(total_rows, p.max_tokens));
+    s.give[p.batch] = whole ? int(total_give) : 0;
+    if (first_cta) p.cu[p.batch] = total_rows;
   }
   __syncthreads();
+  const int taken = s_taken, given = s.give[p.batch];
 
-  for (int64_t t = tid; t < p.max_tokens; t += kThreads) {
-    int64_t slot = -1;
-    if (whole && t < total_rows) {
-      int lo = 0, hi = p.batch - 1;   // the request with s_row[b] <= t < s_row[b + 1]
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s_row[mid] <= t) lo = mid; else hi = mid - 1;
+  const int lane = tid & 31;
+  const int warps = int(gridDim.x) * kWarps, warp = int(blockIdx.x) * kWarps + (tid >> 5);
+  const auto page_of_new = [&](int b, int k) {   // the k-th page that request b takes
+    return p.ring[wrap(head + s.need[b] + k, p.num_pages)];
+  };
+
+  // Slots, in runs of whole 32s per warp.
+  if (p.phases & kFill) {
+    const int64_t run = ((p.max_tokens + warps - 1) / warps + 31) / 32 * 32;
+    const int64_t end = min(run * (warp + 1), p.max_tokens);
+    const int used = s.row[p.batch];
+    int64_t t = run * warp + lane;
+    int b = t < used ? owner_of(s.row, p.batch, int(t)) : p.batch - 1;
+#pragma unroll 2
+    for (; t < end; t += 32) {
+      int64_t slot = -1;
+      if (t < used) {
+        while (b + 1 < p.batch && s.row[b + 1] <= t) ++b;
+        if (s.granted[b]) {
+          const int pos = s.len[b] + int(t) - s.row[b];
+          const int idx = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page_size;
+          const int page = idx < s.have[b] ? p.table[b * p.table_stride + idx]
+                                           : page_of_new(b, idx - s.have[b]);
+          if (page >= 0 && page < p.num_pages)
+            slot = int64_t(page) * p.page_size + (pos - idx * p.page_size);
+          else
+            err |= FA_PAGED_BAD_PAGE;
+        }
       }
-      if (s_kind[lo] == 1) {
-        const int pos = int(s_len[lo] + t - s_row[lo]);
-        const int page = p.table[lo * p.table_stride + pos / p.page_size];
-        if (page >= 0 && page < p.num_pages)
-          slot = int64_t(page) * p.page_size + pos % p.page_size;
-        else
-          err |= FA_PAGED_BAD_PAGE;
+      p.slots[t] = slot;
+    }
+  }
+  // Pages taken, then pages given back, as one list.
+  if (whole && (p.phases & kFill)) {
+    const int64_t items = int64_t(taken) + given;
+    const int64_t run = ((items + warps - 1) / warps + 31) / 32 * 32;
+    const int64_t end = min(run * (warp + 1), items);
+    const int64_t tail = wrap(head + count, p.num_pages);
+    int bt = -1, bg = -1;
+#pragma unroll 2
+    for (int64_t at = run * warp + lane; at < end; at += 32) {
+      if (at < taken) {
+        const int i = int(at);
+        if (bt < 0) bt = owner_of(s.need, p.batch, i);
+        while (bt + 1 < p.batch && s.need[bt + 1] <= i) ++bt;
+        const int k = i - s.need[bt];
+        p.table[bt * p.table_stride + s.have[bt] + k] = page_of_new(bt, k);
+      } else {
+        const int i = int(at - taken);
+        if (bg < 0) bg = owner_of(s.give, p.batch, i);
+        while (bg + 1 < p.batch && s.give[bg + 1] <= i) ++bg;
+        // It gives back its last pages.
+        const int left = s.have[bg] - (s.give[bg + 1] - s.give[bg]);
+        p.ring[wrap(tail + i, p.num_pages)] =
+            p.table[bg * p.table_stride + left + (i - s.give[bg])];
       }
     }
-    p.slots[t] = slot;
   }
+  if (p.phases & kCommit) {
+    if (!(p.phases & kFill)) asm volatile("griddepcontrol.wait;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = tid * kPerThread + i;
-    if (b < p.batch) p.lens_out[b] = whole && s_kind[b] ? a[i].target : len[i];
+    for (int i = 0; i < kMaxPer; ++i) {
+      const int b = tid * per + i;
+      const bool shrinks = delta[i] < 0 && len[i] >= 0 && len[i] <= most;
+      const bool moved = whole && (granted[i] || shrinks);
+      if (i < per && b < p.batch) p.lens_out[b] = moved ? target[i] : len[i];
+    }
+    if (tid == 0) {
+      p.state_out[0] = whole ? (head + taken) % p.num_pages : head;
+      p.state_out[1] = whole ? count - taken + given : count;
+    }
   }
-  if (tid == 0) {
-    p.state_out[0] = whole ? (head + taken) % p.num_pages : head;
-    p.state_out[1] = whole ? count - taken + total_give : count;
-  }
-  if (err && p.error) atomicOr(p.error, err);
+  if (err && p.error && (p.phases & kFill)) atomicOr(p.error, err);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_plan(const PlanParams &p, cudaStream_t s) {
-  plan_kernel<<<1, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_paged_plan(const PlanParams &p0, cudaStream_t s) {
+  PlanParams p = p0;
+  // Items of work that the host can see: rows, and the pages that requests may
+  // give back.  One CTA does 32768 in about the time of a second launch.
+  const int64_t items = p.max_tokens + int64_t(p.batch) * p.max_pages;
+  p.phases = kFill | kCommit;
+  if (items <= 32768) {
+    plan_kernel<<<1, kThreads, 0, s>>>(p);
+    return cudaGetLastError();
+  }
+  p.phases = kFill;
+  const int64_t ctas = (items + 4 * kThreads - 1) / (4 * kThreads);
+  plan_kernel<<<unsigned(ctas < 152 ? ctas : 152), kThreads, 0, s>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  p.phases = kCommit;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, plan_kernel, p);
 }
 
 }  // namespace fav

@@ -5,39 +5,83 @@
 namespace fav {
 namespace {
 
-// One element of V per (token, head, position); V is the widest type that
-// divides the rows' alignment.
+constexpr int kThreads = 256;
+
 template <typename V>
-__global__ void __launch_bounds__(256) write_kernel(WriteParams p, int esize) {
-  const int per = int(sizeof(V)) / esize;         // elements per V
-  const int row_v = p.d / per;                    // V per head row
-  const int64_t n = int64_t(p.tokens) * p.n_kv * row_v;
-  for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < n;
-       i += int64_t(gridDim.x) * blockDim.x) {
-    const int64_t t = i / (p.n_kv * row_v);
-    const int r = int(i - t * (p.n_kv * row_v));
-    const int h = r / row_v, c = r - h * row_v;
+__device__ __forceinline__ V load_once(const V *p) {
+  return *p;
+}
+template <>
+__device__ __forceinline__ uint4 load_once<uint4>(const uint4 *p) {
+  return __ldcs(p);
+}
+
+// A copy: a thread takes U pieces (of type V, the widest that divides every
+// row's alignment) of K and of V, kThreads apart, and has all its loads on the
+// way before the first store.  Pieces are numbered token by token, so that a
+// token's row is read, and where the layout allows written, in one sweep.
+template <typename V, int U>
+__global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ WriteParams p,
+                                                         int esize) {
+  const int per = int(sizeof(V)) / esize;         // elements per piece
+  const unsigned head_v = p.d / per;              // pieces per head
+  const unsigned row_v = p.n_kv * head_v;         // ... and per token
+  const int64_t first = int64_t(blockIdx.x) * (kThreads * U);
+  // Token and piece of the block's first one; the others follow in 32 bits.
+  const int64_t t0 = first / row_v;
+  const unsigned r0 = unsigned(first - t0 * row_v) + threadIdx.x;
+  V k[U], v[U];
+  int64_t to[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const unsigned i = r0 + u * kThreads;
+    const unsigned dt = i / row_v, r = i - dt * row_v;
+    const int64_t t = t0 + dt;
+    to[u] = -1;
+    if (t >= p.tokens) continue;
     const int64_t slot = p.slots[t];
     if (slot < 0) continue;
     if (slot >= p.n_slots) {
       if (p.error && r == 0) atomicOr(p.error, FA_PAGED_BAD_SLOT);
       continue;
     }
-    const int64_t page = slot / p.page_size, tok = slot - page * p.page_size;
-    const int64_t to =
-        (page * p.page_stride + tok * p.token_stride + h * p.head_stride) / per + c;
-    static_cast<V *>(p.kc)[to] = static_cast<const V *>(p.k)[t * p.k_stride / per + r];
-    static_cast<V *>(p.vc)[to] = static_cast<const V *>(p.v)[t * p.v_stride / per + r];
+    int64_t page, tok;
+    if (p.page_shift >= 0) {
+      page = slot >> p.page_shift;
+      tok = slot & (p.page_size - 1);
+    } else if (slot <= 0xffffffffll) {
+      page = uint32_t(slot) / uint32_t(p.page_size);
+      tok = slot - page * p.page_size;
+    } else {
+      page = slot / p.page_size;
+      tok = slot - page * p.page_size;
+    }
+    const unsigned h = r / head_v, c = r - h * head_v;
+    to[u] = (page * p.page_stride + tok * p.token_stride + h * p.head_stride) / per + c;
+    k[u] = load_once(static_cast<const V *>(p.k) + (t * p.k_stride / per + r));
+    v[u] = load_once(static_cast<const V *>(p.v) + (t * p.v_stride / per + r));
   }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (to[u] < 0) continue;
+    static_cast<V *>(p.kc)[to[u]] = k[u];
+    static_cast<V *>(p.vc)[to[u]] = v[u];
+  }
+}
+
+template <typename V, int U>
+cudaError_t launch_u(const WriteParams &p, int esize, int64_t pieces, cudaStream_t s) {
+  const int64_t blocks = (pieces + kThreads * U - 1) / (kThreads * U);
+  write_kernel<V, U><<<unsigned(blocks), kThreads, 0, s>>>(p, esize);
+  return cudaGetLastError();
 }
 
 template <typename V>
 cudaError_t launch(const WriteParams &p, int esize, cudaStream_t s) {
-  const int64_t n = int64_t(p.tokens) * p.n_kv * (p.d * esize / int(sizeof(V)));
-  int64_t blocks = (n + 255) / 256;
-  if (blocks > 152 * 64) blocks = 152 * 64;
-  write_kernel<V><<<int(blocks), 256, 0, s>>>(p, esize);
-  return cudaGetLastError();
+  const int64_t pieces = int64_t(p.tokens) * p.n_kv * (p.d * esize / int(sizeof(V)));
+  // Few rows: one piece per thread, to spread them over the SMs.
+  if (pieces <= 152 * kThreads * 4) return launch_u<V, 1>(p, esize, pieces, s);
+  return launch_u<V, 4>(p, esize, pieces, s);
 }
 
 }  // namespace
