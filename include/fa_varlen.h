@@ -462,11 +462,13 @@ fa_status fa_paged_write(const void *k, const void *v, int64_t k_stride, int64_t
                          int64_t head_stride, fa_dtype dtype, int32_t *error,
                          fa_stream_t stream);
 
-/* Workspace of fa_paged_decode in bytes, on the current device.  It does not
- * depend on the lengths.  A workspace serves one call at a time: calls that
- * may overlap (other streams, graphs replayed at once) need one each. */
+/* Workspace of fa_paged_decode in bytes (0: it needs none), on the current
+ * device, from the same scalars.  It does not depend on the lengths.  A
+ * workspace serves one call at a time: calls that may overlap (other streams,
+ * graphs replayed at once) need one each. */
 fa_status fa_paged_decode_workspace_size(int64_t batch, int64_t head_num, int64_t head_num_kv,
-                                         int64_t head_dim, fa_dtype dtype,
+                                         int64_t head_dim, fa_dtype dtype, int64_t page_size,
+                                         int64_t max_pages, int64_t pre_tokens,
                                          size_t *workspace_bytes);
 
 /* Attention of one query row per request: row b of q ([batch, head_num,
@@ -481,7 +483,9 @@ fa_status fa_paged_decode_workspace_size(int64_t batch, int64_t head_num, int64_
  * A request with no key to see (length 0, or pre_tokens < 0), or whose every
  * score is -inf, gets y = 0, max = -inf, sum = 0.  What the cache holds behind
  * a request's length, infinities and NaN too, has no influence.  The result
- * does not change from run to run on one device (fixed add order). */
+ * does not change from run to run on one device (fixed add order).
+ * workspace: 16-byte aligned (FA_ERR_INVALID otherwise), at least what
+ * fa_paged_decode_workspace_size gives; NULL where that is 0. */
 fa_status fa_paged_decode(const void *q, int64_t q_stride, const void *k_pages,
                           const void *v_pages, int64_t num_pages, int64_t page_size,
                           int64_t page_stride, int64_t token_stride, int64_t head_stride,

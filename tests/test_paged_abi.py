@@ -87,8 +87,7 @@ def test_write_of_nothing_launches_nothing():
     assert call("fa_paged_write", WRITE, tokens=0, page_size=0) == fa.FA_ERR_INVALID
 
 
-@pytest.mark.parametrize("null", ["q", "k_pages", "v_pages", "block_table", "seq_lens", "y",
-                                  "workspace"])
+@pytest.mark.parametrize("null", ["q", "k_pages", "v_pages", "block_table", "seq_lens", "y"])
 def test_decode_null(null):
     assert call("fa_paged_decode", DECODE, **{null: None}) == fa.FA_ERR_NULLPTR
 
@@ -110,14 +109,24 @@ def test_decode_invalid(bad):
 
 def test_decode_workspace():
     out = ctypes.c_size_t(0)
-    size = fa.lib().fa_paged_decode_workspace_size
-    assert size(4, 8, 4, 128, 2, ctypes.byref(out)) == fa.FA_OK and out.value > 0
-    assert call("fa_paged_decode", DECODE, workspace_bytes=out.value - 1) == fa.FA_ERR_WORKSPACE
-    assert size(4, 8, 4, 128, 2, None) == fa.FA_ERR_NULLPTR
-    assert size(0, 8, 4, 128, 2, ctypes.byref(out)) == fa.FA_ERR_INVALID
-    assert size(4, 8, 3, 128, 2, ctypes.byref(out)) == fa.FA_ERR_INVALID
-    assert size(4, 8, 4, 128, 9, ctypes.byref(out)) == fa.FA_ERR_INVALID
-    assert size(4, 8, 4, 80, 2, ctypes.byref(out)) == fa.FA_ERR_UNSUPPORTED
+
+    def size(batch=4, head_num=8, head_num_kv=4, head_dim=128, dtype=2, page_size=16,
+             max_pages=4096, pre_tokens=BIG, out=ctypes.byref(out)):
+        return fa.lib().fa_paged_decode_workspace_size(batch, head_num, head_num_kv, head_dim,
+                                                       dtype, page_size, max_pages, pre_tokens, out)
+    long = dict(max_pages=4096, table_stride=4096)
+    assert size() == fa.FA_OK and out.value > 0
+    assert call("fa_paged_decode", DECODE, workspace_bytes=out.value - 1, **long) == \
+        fa.FA_ERR_WORKSPACE
+    assert call("fa_paged_decode", DECODE, workspace=None, **long) == fa.FA_ERR_NULLPTR
+    # few short requests need none
+    assert size(max_pages=8) == fa.FA_OK and out.value == 0
+    assert size(pre_tokens=100) == fa.FA_OK and out.value == 0
+    assert size(out=None) == fa.FA_ERR_NULLPTR
+    for bad in (dict(batch=0), dict(batch=2049), dict(head_num_kv=3), dict(dtype=9),
+                dict(page_size=0), dict(max_pages=0), dict(max_pages=2 ** 27)):
+        assert size(**bad) == fa.FA_ERR_INVALID
+    assert size(head_dim=80) == fa.FA_ERR_UNSUPPORTED
 
 
 def test_binding_refuses_host_tensors():

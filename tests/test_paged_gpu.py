@@ -189,17 +189,26 @@ def run_decode(dtype, lens, heads, heads_kv, dim, page, layout="NHD", window=BIG
     if edit:
         edit(table, cache[0], cache[1], lens)
     scale = dim ** -0.5 if scale is None else scale
-    ref = oracle.paged_decode(f64(q), f64(cache[0]), f64(cache[1]), table, lens, scale, window)
     kd, vd = to_device(cache, DEV)
-    ws = torch.full((fa.paged_decode_workspace_size(len(lens), heads, heads_kv, dim, q.dtype),), 255,
-                    dtype=torch.uint8, device=DEV)
-    err = torch.zeros(1, dtype=torch.int32, device=DEV)
-    args = (q.to(DEV), kd, vd, dev(table, torch.int32), dev(lens, torch.int32), scale)
-    y, top, total = fa.paged_decode(*args, pre_tokens=window, stats=True, workspace=ws, error=err)
-    check_decode(ref, v_max, dim, dtype, y, top, total)
-    assert int(err) == ref["error"]
-    again, none, _ = fa.paged_decode(*args, pre_tokens=window)
-    assert none is None and np.array_equal(f64(again), f64(y), equal_nan=True)
+    qd, lens_d = q.to(DEV), dev(lens, torch.int32)
+    # Once with the table as wide as the longest request, where few and short
+    # requests are run directly, and once with a wide one, where all are cut into
+    # ranges and joined.
+    wide = np.full((len(lens), max(table.shape[1], 40000 // page)), -1, np.int32)
+    wide[:, :table.shape[1]] = table
+    for tab in (table, wide):
+        ref = oracle.paged_decode(f64(q), f64(cache[0]), f64(cache[1]), tab, lens, scale, window)
+        size = fa.paged_decode_workspace_size(len(lens), heads, heads_kv, dim, q.dtype, page,
+                                              tab.shape[1], window)
+        ws = torch.full((size,), 255, dtype=torch.uint8, device=DEV)
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        args = (qd, kd, vd, dev(tab, torch.int32), lens_d, scale)
+        y, top, total = fa.paged_decode(*args, pre_tokens=window, stats=True, workspace=ws,
+                                        error=err)
+        check_decode(ref, v_max, dim, dtype, y, top, total)
+        assert int(err) == ref["error"]
+        again, none, _ = fa.paged_decode(*args, pre_tokens=window)
+        assert none is None and np.array_equal(f64(again), f64(y), equal_nan=True)
     return y
 
 
@@ -496,8 +505,10 @@ def test_refusals_on_the_device():
                 dict(error=torch.zeros(1, dtype=torch.int64, device=DEV))):
         with pytest.raises(ValueError):
             fa.paged_decode(*a, **bad)
+    wide = torch.full((2, 4096), -1, dtype=torch.int32, device=DEV)
     with pytest.raises(fa.FaError, match="WORKSPACE"):
-        fa.paged_decode(*a, workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
+        fa.paged_decode(q, k, v, wide, lens, scale,
+                        workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
     with pytest.raises(ValueError):
         fa.paged_decode(q.float(), k, v, table, lens, scale)
     with pytest.raises(ValueError):

@@ -92,7 +92,7 @@ _SIGS = {
                        _vp, _vp, _vp], _i32),
     "fa_paged_write": ([_vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp] + [_i64] * 7 +
                        [_i32, _vp, _vp], _i32),
-    "fa_paged_decode_workspace_size": ([_i64, _i64, _i64, _i64, _i32, _psz], _i32),
+    "fa_paged_decode_workspace_size": ([_i64] * 4 + [_i32] + [_i64] * 3 + [_psz], _i32),
     "fa_paged_decode": ([_vp, _i64, _vp, _vp] + [_i64] * 5 + [_vp, _i64, _i64, _vp] + [_i64] * 4 +
                         [_i32, _f64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
 }
@@ -544,19 +544,21 @@ def paged_write(k, v, slots, k_pages, v_pages, error=None, stream=None):
         _check(status, "fa_paged_write")
 
 
-def paged_decode_workspace_size(batch, n, n_kv, d, dtype) -> int:
+def paged_decode_workspace_size(batch, n, n_kv, d, dtype, page_size, max_pages,
+                                pre_tokens=2 ** 31 - 1) -> int:
     """Bytes of the workspace of ``paged_decode`` on the current device."""
     out = ctypes.c_size_t(0)
-    _check(lib().fa_paged_decode_workspace_size(int(batch), int(n), int(n_kv), int(d),
-                                                _DTYPE[dtype], ctypes.byref(out)),
-           "fa_paged_decode_workspace_size")
+    _check(lib().fa_paged_decode_workspace_size(
+        int(batch), int(n), int(n_kv), int(d), _DTYPE[dtype], int(page_size), int(max_pages),
+        min(max(int(pre_tokens), -1), 2 ** 40), ctypes.byref(out)),
+        "fa_paged_decode_workspace_size")
     return out.value
 
 
 @functools.lru_cache(maxsize=256)
-def _decode_workspace(index, batch, n, n_kv, d, dtype):
+def _decode_workspace(index, *call):
     """paged_decode_workspace_size of a call on device `index`, the current one."""
-    return paged_decode_workspace_size(batch, n, n_kv, d, dtype)
+    return paged_decode_workspace_size(*call)
 
 
 def paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, pre_tokens=2 ** 31 - 1,
@@ -593,20 +595,24 @@ def paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, pre_tokens=2
                     t.get_device() == index):
                 _refuse(name, t, f"contiguous fp32 {(b, n, 8)}", index)
         top, total = softmax_max.data_ptr(), softmax_sum.data_ptr()
+    at_workspace = None
     if workspace is None:
-        nbytes = _decode_workspace(index, b, n, n_kv, d, dtype)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        nbytes = _decode_workspace(index, b, n, n_kv, d, dtype, shape[1], max_pages, pre_tokens)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            at_workspace = workspace.data_ptr()
     else:
         nbytes = workspace.numel() * workspace.element_size()
         if not (workspace.is_contiguous() and workspace.get_device() == index):
             _refuse("workspace", workspace, "contiguous memory", index)
+        at_workspace = workspace.data_ptr()
     status = (_LIB or lib()).fa_paged_decode(
         q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), shape[0], shape[1], strides[0],
         strides[1], strides[2], block_table.data_ptr(), max_pages, table_stride,
         _flat(seq_lens, torch.int32, b, index, "seq_lens"), b, n, n_kv, d, _DTYPE[dtype], scale,
         min(max(int(pre_tokens), -1), 2 ** 40), y.data_ptr(), ys, top, total,
         None if error is None else _flat(error, torch.int32, 1, index, "error"),
-        workspace.data_ptr(), nbytes, _raw_stream(index))
+        at_workspace, nbytes, _raw_stream(index))
     if status:
         _check(status, "fa_paged_decode")
     return y, softmax_max, softmax_sum

@@ -53,16 +53,21 @@ struct DecodeParams {
   int max_pages, batch, n, n_kv, d, group;
   int q_pairs, y_pairs;   // rows of q, y start on 4-byte boundaries
   int pre;            // pre_tokens clamped to [-1, 2^30]
+  int rows, direct;   // DecodePlan
   int grid;           // CTAs of the main kernel
   int ranges;         // its warps
   int unit_shift;     // log2 of the blocks in a unit of work
   float scale, scale_log2;
 };
 
-// Most warps of a CTA of the main kernel, one CTA per SM.
-constexpr int kDecodeWarps = 8;
-// Query heads of one key head that a CTA takes at a time.
-int decode_rows(fa_dtype dt, int group);
+// How a decode call is run.
+struct DecodePlan {
+  int rows;     // query heads of one key head that a warp takes at a time
+  int warps;    // per CTA
+  int direct;   // CTAs per segment (see paged_decode.cu), or 0: ranges and a join
+};
+DecodePlan decode_plan(fa_dtype dt, int batch, int n_kv, int group, int d, int64_t max_keys,
+                       int sms);
 // Floats of one partial result in the workspace.
 size_t decode_part_floats(int rows, int d);
 

@@ -102,13 +102,20 @@ struct DecodeLayout {
   size_t part, warp_part, total;
 };
 
-DecodeLayout decode_layout(int ctas, int rows, int64_t head_dim) {
+// Two partial results per CTA and one per warp; none for a direct call.
+DecodeLayout decode_layout(const DecodePlan &plan, int ctas, int64_t head_dim) {
+  const size_t slot = decode_part_floats(plan.rows, int(head_dim)) * sizeof(float);
   DecodeLayout L;
   L.part = 0;
-  const size_t slot = decode_part_floats(rows, int(head_dim)) * sizeof(float);
-  L.warp_part = L.part + align_up(size_t(ctas) * 2 * slot);
-  L.total = L.warp_part + align_up(size_t(ctas) * kDecodeWarps * slot);
+  L.warp_part = align_up(size_t(ctas) * 2 * slot);
+  L.total = plan.direct ? 0 : L.warp_part + align_up(size_t(ctas) * plan.warps * slot);
   return L;
+}
+
+// Keys that a query can see at most.
+int64_t most_keys(int64_t max_pages, int64_t page_size, int64_t pre_tokens) {
+  const int64_t keys = max_pages * page_size;
+  return pre_tokens < 0 ? 0 : pre_tokens < keys ? pre_tokens + 1 : keys;
 }
 
 }  // namespace
@@ -195,14 +202,19 @@ fa_status fa_paged_write(const void *k, const void *v, int64_t k_stride, int64_t
 }
 
 fa_status fa_paged_decode_workspace_size(int64_t batch, int64_t head_num, int64_t head_num_kv,
-                                         int64_t head_dim, fa_dtype dtype,
+                                         int64_t head_dim, fa_dtype dtype, int64_t page_size,
+                                         int64_t max_pages, int64_t pre_tokens,
                                          size_t *workspace_bytes) {
   if (!workspace_bytes) return FA_ERR_NULLPTR;
-  if (batch < 1 || batch > kMaxBatch) return FA_ERR_INVALID;
-  const fa_status st = check_heads(head_num, head_num_kv, head_dim, dtype);
+  fa_status st = check_table(batch, 1, page_size, max_pages, max_pages);
   if (st != FA_OK) return st;
-  const int rows = decode_rows(dtype, int(head_num / head_num_kv));
-  *workspace_bytes = decode_layout(sm_count(), rows, head_dim).total;
+  st = check_heads(head_num, head_num_kv, head_dim, dtype);
+  if (st != FA_OK) return st;
+  const int sms = sm_count();
+  const DecodePlan plan = decode_plan(dtype, int(batch), int(head_num_kv),
+                                      int(head_num / head_num_kv), int(head_dim),
+                                      most_keys(max_pages, page_size, pre_tokens), sms);
+  *workspace_bytes = decode_layout(plan, sms, head_dim).total;
   return FA_OK;
 }
 
@@ -215,7 +227,7 @@ fa_status fa_paged_decode(const void *q, int64_t q_stride, const void *k_pages,
                           int64_t pre_tokens, void *y, int64_t y_stride, float *softmax_max,
                           float *softmax_sum, int32_t *error, void *workspace,
                           size_t workspace_bytes, fa_stream_t stream) {
-  if (!q || !k_pages || !v_pages || !block_table || !seq_lens || !y || !workspace ||
+  if (!q || !k_pages || !v_pages || !block_table || !seq_lens || !y ||
       (!softmax_max != !softmax_sum))
     return FA_ERR_NULLPTR;
   fa_status st = check_heads(head_num, head_num_kv, head_dim, dtype);
@@ -229,10 +241,14 @@ fa_status fa_paged_decode(const void *q, int64_t q_stride, const void *k_pages,
   const int64_t row = head_num * head_dim;
   if (bad_rows(q_stride, batch, row) || bad_rows(y_stride, batch, row)) return FA_ERR_INVALID;
   if (!element_aligned(q, dtype) || !element_aligned(y, dtype)) return FA_ERR_INVALID;
-  if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return FA_ERR_INVALID;
   const int sms = sm_count();
   const int group = int(head_num / head_num_kv);
-  const DecodeLayout L = decode_layout(sms, decode_rows(dtype, group), head_dim);
+  const DecodePlan plan =
+      decode_plan(dtype, int(batch), int(head_num_kv), group, int(head_dim),
+                  most_keys(max_pages, page_size, pre_tokens), sms);
+  const DecodeLayout L = decode_layout(plan, sms, head_dim);
+  if (L.total > 0 && !workspace) return FA_ERR_NULLPTR;
+  if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return FA_ERR_INVALID;
   if (workspace_bytes < L.total) return FA_ERR_WORKSPACE;
 
   DecodeParams p{};
@@ -262,6 +278,8 @@ fa_status fa_paged_decode(const void *q, int64_t q_stride, const void *k_pages,
   p.n_kv = int(head_num_kv);
   p.d = int(head_dim);
   p.group = group;
+  p.rows = plan.rows;
+  p.direct = plan.direct;
   const auto pairs = [](const void *ptr, int64_t stride) {
     return reinterpret_cast<uintptr_t>(ptr) % 4 == 0 && stride % 2 == 0;
   };

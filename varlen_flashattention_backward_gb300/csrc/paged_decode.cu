@@ -16,6 +16,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kFull = 0xffffffffu;
 // Beginning a segment costs a warp about as much as this many blocks of keys.
 constexpr int kSwitchBlocks = 1;
+// Most CTAs of a cluster that shares a segment, and blocks for each warp of it.
+constexpr int kMaxDirect = 8;
+constexpr int kDirectBlocks = 4;
 
 // ---------------------------------------------------------------------------
 // Division of the work
@@ -34,6 +37,11 @@ constexpr int kSwitchBlocks = 1;
 // parts of one segment are added.  What then still misses a neighbour, at most
 // two sums per CTA, goes to the workspace: slot 0 where it does not begin its
 // segment, slot 1 where it does.  join_kernel adds those, in order.
+//
+// Where there are few segments and none can be long (direct_ctas), a segment
+// gets a cluster of CTAs instead: its blocks are dealt to their warps, and the
+// CTAs' sums are added through distributed shared memory.  That saves finding
+// the ranges, the workspace and the second kernel.
 // ---------------------------------------------------------------------------
 struct Span {
   int lo, hi;        // keys [lo, hi) that the query sees
@@ -186,8 +194,8 @@ enum : int {
   kDone = 1 << 21          // no block: the range is done
 };
 
-// Shared memory of one kernel: NW rings of S stages (K and V block each), then
-// what the kernel adds per warp.  Three stages of eight warps keep 128 KB on
+// Shared memory of one kernel: NW rings of S stages (K and V block each), what
+// the kernel adds per warp, and one partial result of the whole CTA.  Three stages of eight warps keep 128 KB on
 // the way, which is what the memory needs; where they do not fit, four warps
 // with more stages are taken if they do better (MINS: the stages that eight
 // warps must have).
@@ -198,11 +206,11 @@ struct Shape {
   static constexpr int kStage = 2 * kBlock;
   static constexpr int kPartial = R * (D + PAD) * 4;
   static constexpr int kExtra = EXTRA;
-  static constexpr int kBudget = 227 * 1024 - 4096;           // 4 KB of static arrays
+  static constexpr int kBudget = 227 * 1024 - 4096 - kPartial;   // 4 KB of static arrays
   static constexpr int fit(int nw) { return (kBudget - nw * kExtra) / (nw * kStage); }
   static constexpr int NW = fit(8) >= MINS ? 8 : 4;
   static constexpr int S = fit(NW) > 8 ? 8 : fit(NW);
-  static constexpr int kSmem = NW * (S * kStage + kExtra);
+  static constexpr int kSmem = NW * (S * kStage + kExtra) + kPartial;
   static_assert(S >= 2 && S * kStage >= kPartial, "decode stages");
 };
 
@@ -230,6 +238,24 @@ struct Loader {
       : p(p), chunks(chunks), segs(p.n_kv * chunks), lane(threadIdx.x & 31), left(0), off(0),
         units(0), b(0), seg(0), blk(0), end(0), begins(false), page(-1), tok(0), head(0), err(0),
         inside(false) {
+    if (p.direct) {
+      const int id = blockIdx.x / p.direct, warps = p.direct * (blockDim.x >> 5);
+      b = id / segs;
+      seg = id - b * segs;
+      head = chunks == 1 ? seg : seg / chunks;
+      const int len = __ldg(p.lens + b);
+      if ((len < 0 || len > p.max_pages * p.page_size) && p.error)
+        atomicOr(p.error, FA_PAGED_BAD_LENGTH);
+      span = span_of<KB>(p, len);
+      const int per = (span.blocks + warps - 1) / warps;
+      const int mine = range - id * warps;
+      blk = min(mine * per, span.blocks);
+      end = min(blk + per, span.blocks);
+      begins = true;
+      desc.y = b;
+      desc.z = seg;
+      return;
+    }
     Line line;
     Place at;
     if (find<KB>(p, segs, range, 0, line, at)) {
@@ -359,7 +385,7 @@ __device__ __forceinline__ float *partial_at(const DecodeParams &p, int rows, bo
 // one run at a time.
 template <typename T, int D, int R, int NW, int PAD>
 __device__ __forceinline__ void merge_partials(const DecodeParams &p, int chunks,
-                                               const Partials<NW, R> &s) {
+                                               const Partials<NW, R> &s, float *cta_part) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = min(R, p.group);
   // Lane k < NW: the id in warp k's slot A, lane 16 + k: in its slot B.
@@ -397,7 +423,7 @@ __device__ __forceinline__ void merge_partials(const DecodeParams &p, int chunks
     const float f = sm103::ex2(m - (mx == -CUDART_INF_F ? 0.f : mx));
     float sum = 0.f;
     const bool whole = slot == 1 && ends;
-    float *dst = slot_of(p, blockIdx.x, slot, R);
+    float *dst = p.direct ? cta_part : slot_of(p, blockIdx.x, slot, R);
 #pragma unroll
     for (int d0 = 0; d0 < D; d0 += 128) {
       const int d = d0 + lane * 4;
@@ -438,6 +464,64 @@ __device__ __forceinline__ void merge_partials(const DecodeParams &p, int chunks
       }
     }
   }
+}
+
+// The sums of a cluster's CTAs, each at `cta_part` of its shared memory, to y.
+// A warp of the cluster takes one row.
+template <typename T, int D, int R, int NW, int KB>
+__device__ __forceinline__ void join_cluster(const DecodeParams &p, int chunks,
+                                             const float *cta_part) {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  const int lane = threadIdx.x & 31, segs = p.n_kv * chunks;
+  const int id = blockIdx.x / p.direct;
+  const int r = (blockIdx.x - id * p.direct) * NW + (threadIdx.x >> 5);
+  const int b = id / segs, seg = id - b * segs;
+  const int h = (chunks == 1 ? 0 : seg % chunks * R) + r;
+  const int blocks = span_of<KB>(p, __ldg(p.lens + b)).blocks;
+  const int per = (blocks + p.direct * NW - 1) / (p.direct * NW);
+  const int parts = (blocks + per * NW - 1) / (per * NW);   // CTAs that have blocks
+  if (parts > 1 && r < R && h < p.group) {
+    const int n = (chunks == 1 ? seg : seg / chunks) * p.group + h;
+    const uint32_t at = sm103::smem_u32(cta_part);
+    const auto remote = [](uint32_t addr, int rank) {
+      uint32_t a;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+      return a;
+    };
+    const auto load = [&](int rank, int i) {
+      float x;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                   : "=f"(x)
+                   : "r"(remote(at + i * 4, rank))
+                   : "memory");
+      return x;
+    };
+    const int mine = lane < parts ? lane : 0;
+    const float m = load(mine, R * D + r), l = load(mine, R * D + R + r);
+    float mx = m;
+#pragma unroll
+    for (int o = 1; o < kMaxDirect; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    const float f = sm103::ex2(m - (mx == -CUDART_INF_F ? 0.f : mx));
+    float sum = 0.f, acc[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      const float fk = __shfl_sync(kFull, f, k);
+      sum += fk * __shfl_sync(kFull, l, k);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) acc[i] += fk * load(k, r * D + lane + 32 * i);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    T *y = static_cast<T *>(p.y) + b * p.y_stride + int64_t(n) * D + lane;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) y[32 * i] = from_f<T>(acc[i] * inv);
+    if (lane == 0) write_stats(p, b, n, mx * kLn2, sum);
+  }
+  // No CTA may leave while another reads its shared memory.
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -730,7 +814,9 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p) {
     }
   }
   __syncthreads();
-  merge_partials<T, D, R, NW, Sh::PAD>(p, chunks, s_part);
+  float *cta_part = reinterpret_cast<float *>(smem + NW * (S * Sh::kStage + Sh::kExtra));
+  merge_partials<T, D, R, NW, Sh::PAD>(p, chunks, s_part, cta_part);
+  if (p.direct > 1) join_cluster<T, D, R, NW, KB>(p, chunks, cta_part);
   if (load.err && p.error) atomicOr(p.error, load.err);
 }
 
@@ -918,7 +1004,9 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p) {
     }
   }
   __syncthreads();
-  merge_partials<float, D, R, NW, Sh::PAD>(p, chunks, s_part);
+  float *cta_part = reinterpret_cast<float *>(smem + NW * (S * Sh::kStage + Sh::kExtra));
+  merge_partials<float, D, R, NW, Sh::PAD>(p, chunks, s_part, cta_part);
+  if (p.direct > 1) join_cluster<float, D, R, NW, KB>(p, chunks, cta_part);
   if (load.err && p.error) atomicOr(p.error, load.err);
 }
 
@@ -1020,27 +1108,36 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(
 // launch overlaps the main kernel's run.
 template <typename T, int D, int R, int KB, int NW, typename Kernel>
 cudaError_t launch_both(DecodeParams p, Kernel kernel, int smem, int sms, cudaStream_t s) {
-  p.grid = sms;
-  p.ranges = sms * NW;
   const int64_t segments = int64_t(p.batch) * p.n_kv * ((p.group + R - 1) / R);
-  const int64_t blocks = (int64_t(p.max_pages) * p.page_size + KB - 1) / KB + 1 + kSwitchBlocks;
-  p.unit_shift = 0;
-  while (segments * ((blocks >> p.unit_shift) + 1) >= (int64_t(1) << 31)) ++p.unit_shift;
   cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (p.direct) {
+    cfg.gridDim = dim3(unsigned(segments) * p.direct);
+    cfg.blockDim = dim3(NW * 32);
+    cfg.dynamicSmemBytes = smem;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = p.direct;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+  }
+  p.grid = sms;
+  p.ranges = sms * NW;
+  const int64_t blocks = (int64_t(p.max_pages) * p.page_size + KB - 1) / KB + 1 + kSwitchBlocks;
+  p.unit_shift = 0;
+  while (segments * ((blocks >> p.unit_shift) + 1) >= (int64_t(1) << 31)) ++p.unit_shift;
   kernel<<<p.grid, NW * 32, smem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int by_segment = segments <= p.grid;
-  cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned(by_segment ? segments : p.grid), unsigned(p.group < R ? p.group : R));
   cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, join_kernel<T, D, KB, NW>, p, R, by_segment);
 }
 
@@ -1072,20 +1169,51 @@ cudaError_t launch_d(const DecodeParams &p, fa_dtype dt, int rows, int sms, cuda
                    : launch_tc<__nv_bfloat16, D, 16>(p, sms, s);
 }
 
+template <int D>
+int warps_of_d(bool tc, int rows) {
+  if (tc) return rows == 8 ? TcShape<D, 8>::NW : TcShape<D, 16>::NW;
+  return rows == 1 ? SimtShape<D, 1>::NW : rows == 2 ? SimtShape<D, 2>::NW
+         : rows == 4 ? SimtShape<D, 4>::NW : SimtShape<D, 8>::NW;
+}
+
+int warps_of(bool tc, int rows, int d) {
+  switch (d) {
+    case 32: return warps_of_d<32>(tc, rows);
+    case 64: return warps_of_d<64>(tc, rows);
+    case 96: return warps_of_d<96>(tc, rows);
+    case 128: return warps_of_d<128>(tc, rows);
+    default: return warps_of_d<192>(tc, rows);
+  }
+}
+
 }  // namespace
 
-// fp32: the heads whose outputs a lane's registers hold at once.  16-bit types:
-// the rows of one product, all 16 of which serve P rounded once a group has
-// more than 8 heads.
-int decode_rows(fa_dtype dt, int group) {
-  if (dt != FA_DTYPE_FP32) return group <= 8 ? 8 : 16;
-  return group <= 1 ? 1 : group <= 2 ? 2 : group <= 4 ? 4 : 8;
+// The shape of a call, from its scalars alone.
+DecodePlan decode_plan(fa_dtype dt, int batch, int n_kv, int group, int d, int64_t max_keys,
+                       int sms) {
+  DecodePlan plan;
+  // fp32: the heads whose outputs a lane's registers hold at once.  16-bit types:
+  // the rows of one product, all 16 of which serve P rounded once a group has
+  // more than 8 heads.
+  const bool tc = dt != FA_DTYPE_FP32;
+  plan.rows = tc ? (group <= 8 ? 8 : 16) : group <= 1 ? 1 : group <= 2 ? 2 : group <= 4 ? 4 : 8;
+  plan.warps = warps_of(tc, plan.rows, d);
+  // The largest cluster per segment that still puts all of them on the GPU at
+  // once, if its warps get at most kDirectBlocks blocks each.
+  const int kb = tc ? 16 : 8;
+  const int64_t blocks = (max_keys + kb - 1) / kb + 1;
+  const int64_t segments = int64_t(batch) * n_kv * ((group + plan.rows - 1) / plan.rows);
+  int ctas = 1;
+  while (ctas < kMaxDirect && segments * ctas * 2 <= sms && ctas * plan.warps < blocks) ctas *= 2;
+  plan.direct =
+      segments * ctas <= sms && blocks <= int64_t(ctas) * plan.warps * kDirectBlocks ? ctas : 0;
+  return plan;
 }
 
 size_t decode_part_floats(int rows, int d) { return size_t(slot_floats(rows, d)); }
 
 cudaError_t launch_paged_decode(const DecodeParams &p, fa_dtype dt, int sms, cudaStream_t s) {
-  const int rows = decode_rows(dt, p.group);
+  const int rows = p.rows;
   switch (p.d) {
     case 32: return launch_d<32>(p, dt, rows, sms, s);
     case 64: return launch_d<64>(p, dt, rows, sms, s);
