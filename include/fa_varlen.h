@@ -397,6 +397,8 @@ fa_status fa_varlen_bwd_schedule_ex(const int64_t *seq_lens_q, const int64_t *se
  *   FA_PAGED_BAD_POOL    plan: head or count outside the ring, or more pages
  *                        given back than it has room for; the call changes
  *                        nothing
+ *   FA_PAGED_TIMEOUT     decode: a bounded in-kernel wait expired; the results
+ *                        are invalid
  *   FA_PAGED_BAD_SLOT    write: a slot at or above num_pages * page_size,
  *                        whose row is skipped
  * Limits (FA_ERR_INVALID): batch in [1, 2048]; num_pages in [1, 2^31);
@@ -410,7 +412,8 @@ enum {
   FA_PAGED_BAD_PAGE = 8,
   FA_PAGED_BAD_LENGTH = 16,
   FA_PAGED_BAD_POOL = 32,
-  FA_PAGED_BAD_SLOT = 64
+  FA_PAGED_BAD_SLOT = 64,
+  FA_PAGED_TIMEOUT = 128
 };
 
 /* Grows and shrinks the requests by delta[b] tokens each (device int32

@@ -22,7 +22,7 @@ FA_BWD_AUTO, FA_BWD_SIMT, FA_BWD_TCGEN05 = 0, 1, 2
 
 # Bits of the paged entry points' error word.
 FA_PAGED_EXHAUSTED, FA_PAGED_ROW_FULL, FA_PAGED_ROWS, FA_PAGED_BAD_PAGE = 1, 2, 4, 8
-FA_PAGED_BAD_LENGTH, FA_PAGED_BAD_POOL, FA_PAGED_BAD_SLOT = 16, 32, 64
+FA_PAGED_BAD_LENGTH, FA_PAGED_BAD_POOL, FA_PAGED_BAD_SLOT, FA_PAGED_TIMEOUT = 16, 32, 64, 128
 
 _DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 

@@ -21,7 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "_build")
 LIB_NAME = "libfavarlen.so"
 SOURCES = ["abi.cpp", "simt.cu", "bwd_sm103.cu", "bwd_sm103_pad.cu", "static_scratch.cu",
-           "paged_abi.cpp", "paged_plan.cu", "paged_write.cu", "paged_decode.cu"]
+           "paged_abi.cpp", "paged_plan.cu", "paged_write.cu",
+           "paged_decode_bf16.cu", "paged_decode_fp16.cu", "paged_decode_fp32.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

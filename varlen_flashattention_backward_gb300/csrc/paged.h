@@ -1,5 +1,5 @@
 // Declarations shared by the paged-cache entry points (paged_abi.cpp) and
-// their kernels (paged_plan.cu, paged_write.cu, paged_decode.cu).
+// their kernels (paged_plan.cu, paged_write.cu, paged_decode.cuh).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -47,15 +47,16 @@ struct DecodeParams {
   int64_t y_stride;
   float *smax, *ssum;
   int32_t *error;
-  float *part;        // partial results: two slots per CTA (see paged_decode.cu)
-  float *warp_part;   // ... and one per warp
+  float *part;        // partial results: two slots per CTA (see paged_decode.cuh)
+  float *team_part;   // ... and one per team
   int num_pages, page_size, page_shift;   // page_shift: log2(page_size), or -1
   int max_pages, batch, n, n_kv, d, group;
-  int q_pairs, y_pairs;   // rows of q, y start on 4-byte boundaries
+  int y_pairs;            // rows of y start on 4-byte boundaries
+  int q_chunks;           // rows of q start on 16-byte boundaries
   int pre;            // pre_tokens clamped to [-1, 2^30]
   int rows, direct;   // DecodePlan
   int grid;           // CTAs of the main kernel
-  int ranges;         // its warps
+  int ranges;         // its teams
   int unit_shift;     // log2 of the blocks in a unit of work
   float scale, scale_log2;
 };
@@ -63,8 +64,8 @@ struct DecodeParams {
 // How a decode call is run.
 struct DecodePlan {
   int rows;     // query heads of one key head that a warp takes at a time
-  int warps;    // per CTA
-  int direct;   // CTAs per segment (see paged_decode.cu), or 0: ranges and a join
+  int teams;    // per CTA
+  int direct;   // CTAs per segment (see paged_decode.cuh), or 0: ranges and a join
 };
 DecodePlan decode_plan(fa_dtype dt, int batch, int n_kv, int group, int d, int64_t max_keys,
                        int sms);
@@ -73,6 +74,8 @@ size_t decode_part_floats(int rows, int d);
 
 cudaError_t launch_paged_plan(const PlanParams &p, cudaStream_t s);
 cudaError_t launch_paged_write(const WriteParams &p, fa_dtype dt, cudaStream_t s);
-cudaError_t launch_paged_decode(const DecodeParams &p, fa_dtype dt, int sms, cudaStream_t s);
+cudaError_t launch_paged_decode_bf16(const DecodeParams &p, int sms, cudaStream_t s);
+cudaError_t launch_paged_decode_fp16(const DecodeParams &p, int sms, cudaStream_t s);
+cudaError_t launch_paged_decode_fp32(const DecodeParams &p, int sms, cudaStream_t s);
 
 }  // namespace fav

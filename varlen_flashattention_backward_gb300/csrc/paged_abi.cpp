@@ -99,16 +99,16 @@ int log2_or_none(int64_t x) {
 }
 
 struct DecodeLayout {
-  size_t part, warp_part, total;
+  size_t part, team_part, total;
 };
 
-// Two partial results per CTA and one per warp; none for a direct call.
+// Two partial results per CTA and one per team; none for a direct call.
 DecodeLayout decode_layout(const DecodePlan &plan, int ctas, int64_t head_dim) {
   const size_t slot = decode_part_floats(plan.rows, int(head_dim)) * sizeof(float);
   DecodeLayout L;
   L.part = 0;
-  L.warp_part = align_up(size_t(ctas) * 2 * slot);
-  L.total = plan.direct ? 0 : L.warp_part + align_up(size_t(ctas) * plan.warps * slot);
+  L.team_part = align_up(size_t(ctas) * 2 * slot);
+  L.total = plan.direct ? 0 : L.team_part + align_up(size_t(ctas) * plan.teams * slot);
   return L;
 }
 
@@ -268,7 +268,7 @@ fa_status fa_paged_decode(const void *q, int64_t q_stride, const void *k_pages,
   p.ssum = softmax_sum;
   p.error = error;
   p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.part);
-  p.warp_part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.warp_part);
+  p.team_part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.team_part);
   p.num_pages = int(num_pages);
   p.page_size = int(page_size);
   p.page_shift = log2_or_none(page_size);
@@ -283,14 +283,17 @@ fa_status fa_paged_decode(const void *q, int64_t q_stride, const void *k_pages,
   const auto pairs = [](const void *ptr, int64_t stride) {
     return reinterpret_cast<uintptr_t>(ptr) % 4 == 0 && stride % 2 == 0;
   };
-  p.q_pairs = pairs(q, q_stride);
+  p.q_chunks = reinterpret_cast<uintptr_t>(q) % 16 == 0 &&
+               q_stride % (dtype == FA_DTYPE_FP32 ? 4 : 8) == 0;
   p.y_pairs = pairs(y, y_stride);
   p.pre = int(pre_tokens < -1 ? -1 : pre_tokens > kMaxKeys ? kMaxKeys : pre_tokens);
   p.scale = float(scale);
   p.scale_log2 = float(scale * 1.4426950408889634);
-  return launch_paged_decode(p, dtype, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? FA_OK
-             : FA_ERR_CUDA;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == FA_DTYPE_FP32   ? launch_paged_decode_fp32(p, sms, cs)
+                        : dtype == FA_DTYPE_FP16 ? launch_paged_decode_fp16(p, sms, cs)
+                                                 : launch_paged_decode_bf16(p, sms, cs);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -1,6 +1,9 @@
 // Attention of one new token per request over the paged cache
 // (fa_paged_decode): S_j = scale q . k_j, P = exp(S - max), y = P V / sum P.
+// Included by one translation unit per type.
+#pragma once
 
+#include <cuda.h>
 #include <math_constants.h>
 
 #include <type_traits>
@@ -16,7 +19,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kFull = 0xffffffffu;
 // Beginning a segment costs a warp about as much as this many blocks of keys.
 constexpr int kSwitchBlocks = 1;
-// Most CTAs of a cluster that shares a segment, and blocks for each warp of it.
+// Most CTAs of a cluster that shares a segment, and blocks for each team of it.
 constexpr int kMaxDirect = 8;
 constexpr int kDirectBlocks = 4;
 
@@ -26,20 +29,21 @@ constexpr int kDirectBlocks = 4;
 // A segment is one request, one key head and up to R of its query heads; its
 // keys are cut into blocks of KB (at least one, which may hold no key).  The
 // segments, each weighing its blocks plus kSwitchBlocks, form a line that is
-// cut into ranges of equal weight, one per warp of the grid.  Weights count in
+// cut into ranges of equal weight, one per team of TW warps of the grid (a team
+// shares its blocks; each of its warps has its own R / TW query heads).  Weights count in
 // units of 2^unit_shift blocks, which the host chooses so that 32 bits hold the
 // line's length; the shift is 0 for any batch that fits a GPU's memory.
 //
-// A warp's share of a segment is a part.  A part that is a whole segment
-// writes y from the warp's registers.  Of the others a warp has at most two,
+// A team's share of a segment is a part.  A part that is a whole segment
+// writes y from the warps' registers.  Of the others a team has at most two,
 // its first (slot A, where it does not begin its segment) and its last (slot B,
-// where it does); they wait until the CTA's warps are done, when neighbouring
+// where it does); they wait until the CTA's teams are done, when neighbouring
 // parts of one segment are added.  What then still misses a neighbour, at most
 // two sums per CTA, goes to the workspace: slot 0 where it does not begin its
 // segment, slot 1 where it does.  join_kernel adds those, in order.
 //
 // Where there are few segments and none can be long (direct_ctas), a segment
-// gets a cluster of CTAs instead: its blocks are dealt to their warps, and the
+// gets a cluster of CTAs instead: its blocks are dealt to their teams, and the
 // CTAs' sums are added through distributed shared memory.  That saves finding
 // the ranges, the workspace and the second kernel.
 // ---------------------------------------------------------------------------
@@ -85,69 +89,69 @@ struct Place {
   int units;         // of each of the request's segments
 };
 
-// Measures the line and finds unit `start(range)` on it.  Every warp that asks
-// works it out for itself from all lengths, a lane taking a 32nd of them: that
-// costs less than meeting other warps would.  False: nothing is there.
+// The units of requests 32 i + lane.
+template <int KB>
+__device__ __forceinline__ int units_at(const DecodeParams &p, int b, bool &bad) {
+  if (b >= p.batch) return 0;
+  const int len = __ldg(p.lens + b);
+  bad |= len < 0 || len > p.max_pages * p.page_size;
+  return units_of(p, span_of<KB>(p, len).blocks);
+}
+
+// Measures the line and finds unit `start(range) - before` on it.  Every warp
+// that asks works it out for itself from all lengths: that costs less than
+// meeting other warps would.  Lane i sums up requests 32 i .. 32 i + 31 (and
+// those 1024 further on), then the warp looks at the 32 that hold the unit.
+// False: nothing is there.  (The indexes are held in bounds for the sake of
+// lengths that change during the call, which is an error of the caller's.)
 template <int KB>
 __device__ __forceinline__ bool find(const DecodeParams &p, int segs, int range, int before,
                                      Line &line, Place &at) {
   const int lane = threadIdx.x & 31;
-  const int per = (p.batch + 31) >> 5;
-  const int b0 = lane * per;
-  const int most = p.max_pages * p.page_size;
-  int sum = 0, units = 0;
+  const int rows = (p.batch + 31) >> 5;            // at most 64
+  int sum[2] = {0, 0};
+  int units = 0;
   bool bad = false;
-#pragma unroll 4
-  for (int i = 0; i < per; ++i) {
-    if (b0 + i < p.batch) {
-      const int len = __ldg(p.lens + b0 + i);
-      bad |= len < 0 || len > most;
-      units = units_of(p, span_of<KB>(p, len).blocks);
-      sum += units;
-    }
+#pragma unroll 8
+  for (int i = 0; i < rows; ++i) {
+    units = units_at<KB>(p, i * 32 + lane, bad);
+    const int all = __reduce_add_sync(kFull, units);
+    if (lane == (i & 31)) sum[i >> 5] = all;
   }
   if (bad && range == 0 && p.error) atomicOr(p.error, FA_PAGED_BAD_LENGTH);
-  sum *= segs;
-  int upto = sum;
+  int upto[2] = {sum[0], sum[1]};
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(kFull, upto, o);
-    if (lane >= o) upto += y;
+    const int x = __shfl_up_sync(kFull, upto[0], o), y = __shfl_up_sync(kFull, upto[1], o);
+    if (lane >= o) {
+      upto[0] += x;
+      upto[1] += y;
+    }
   }
-  const int total = __shfl_sync(kFull, upto, 31);
+  upto[1] += __shfl_sync(kFull, upto[0], 31);
+  const int total = __shfl_sync(kFull, upto[1], 31) * segs;
   line.each = total / p.ranges;
   line.rest = total - line.each * p.ranges;
   const int u = line.start(range) - before;
   if (u < 0 || u >= total) return false;
-  // The lane, then the request, inside which u falls.
-  const int owner = __popc(__ballot_sync(kFull, upto <= u));
-  int from = __shfl_sync(kFull, upto - sum, owner);
-  at.b = owner * per;
-  at.units = __shfl_sync(kFull, units, owner);
-  if (per > 1) {
-    for (int i = 0; i < per; i += 32) {
-      const int b = owner * per + i + lane;
-      const int w = i + lane < per && b < p.batch
-                        ? units_of(p, span_of<KB>(p, __ldg(p.lens + b)).blocks)
-                        : 0;
-      int x = w * segs;
+  // The row of requests that holds u, then the request.
+  const int row = __popc(__ballot_sync(kFull, upto[0] * segs <= u)) +
+                  __popc(__ballot_sync(kFull, upto[1] * segs <= u));
+  int from = row < 32 ? __shfl_sync(kFull, upto[0] - sum[0], row)
+                      : __shfl_sync(kFull, upto[1] - sum[1], row - 32);
+  if (rows > 1) units = units_at<KB>(p, row * 32 + lane, bad);
+  int x = units;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(kFull, x, o);
-        if (lane >= o) x += y;
-      }
-      const int n = __popc(__ballot_sync(kFull, from + x <= u));
-      if (n < 32) {
-        at.b = owner * per + i + n;
-        at.units = __shfl_sync(kFull, w, n);
-        from += __shfl_sync(kFull, x, n) - at.units * segs;
-        break;
-      }
-      from += __shfl_sync(kFull, x, 31);
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
   }
-  at.seg = (u - from) / at.units;
-  at.off = u - from - at.seg * at.units;
+  const int n = min(__popc(__ballot_sync(kFull, (from + x) * segs <= u)), 31);
+  at.b = min(row * 32 + n, p.batch - 1);
+  at.units = max(__shfl_sync(kFull, units, n), 1);
+  from += __shfl_sync(kFull, x, n) - at.units;
+  at.seg = min(max((u - from * segs) / at.units, 0), segs - 1);
+  at.off = max(u - from * segs - at.seg * at.units, 0);
   return true;
 }
 
@@ -157,8 +161,9 @@ template <int KB>
 __device__ __forceinline__ int segment_start(const DecodeParams &p, int segs, Place &at,
                                              Line &line) {
   int sum = 0, before = 0;
+  bool bad = false;
   for (int b = threadIdx.x & 31; b < p.batch; b += 32) {
-    const int units = units_of(p, span_of<KB>(p, __ldg(p.lens + b)).blocks);
+    const int units = units_at<KB>(p, b, bad);
     sum += units;
     if (b < at.b) before += units;
   }
@@ -194,37 +199,104 @@ enum : int {
   kDone = 1 << 21          // no block: the range is done
 };
 
-// Shared memory of one kernel: NW rings of S stages (K and V block each), what
-// the kernel adds per warp, and one partial result of the whole CTA.  Three stages of eight warps keep 128 KB on
-// the way, which is what the memory needs; where they do not fit, four warps
-// with more stages are taken if they do better (MINS: the stages that eight
-// warps must have).
-template <typename T, int D, int R, int KB, int EXTRA, int MINS>
+// Shared memory of one kernel of NW warps: a ring of S stages (K and V block
+// each) per team, then per warp QS places for query rows that wait for their
+// part and kExtra bytes more.  The sum of the whole CTA takes the latter's
+// place in the end.  Query rows are fetched ahead where that leaves three
+// stages: under load a fetch takes 1 to 2 us, which a warp would spend waiting at
+// each of its parts.
+template <typename T, int D, int RW, int TW, int KB, int EXTRA>
 struct Shape {
+  static constexpr int R = RW * TW;
   static constexpr int PAD = 4;
-  static constexpr int kBlock = KB * D * int(sizeof(T));      // K or V block of one warp
+  static constexpr int kBlock = KB * D * int(sizeof(T));      // K or V block
   static constexpr int kStage = 2 * kBlock;
   static constexpr int kPartial = R * (D + PAD) * 4;
-  static constexpr int kExtra = EXTRA;
-  static constexpr int kBudget = 227 * 1024 - 4096 - kPartial;   // 4 KB of static arrays
-  static constexpr int fit(int nw) { return (kBudget - nw * kExtra) / (nw * kStage); }
-  static constexpr int NW = fit(8) >= MINS ? 8 : 4;
-  static constexpr int S = fit(NW) > 8 ? 8 : fit(NW);
-  static constexpr int kSmem = NW * (S * kStage + kExtra) + kPartial;
-  static_assert(S >= 2 && S * kStage >= kPartial, "decode stages");
+  static constexpr int kQ = RW * D * int(sizeof(T));
+  // The kernels' static arrays, in the steps of the ring's alignment.
+  static constexpr int static_bytes(int nw, int s) {
+    const int nt = nw / TW;
+    return (nt * (R * 16 + 32) + nw * s * 16 + nt * s * 8 + 64 + 1023) / 1024 * 1024;
+  }
+  // Most stages, up to 8, that fit.
+  static constexpr int fit(int nw, int qs) {
+    int s = 8;
+    while (s > 0 && nw / TW * s * kStage + nw * (qs * kQ + EXTRA) + static_bytes(nw, s) > 227 * 1024)
+      --s;
+    return s;
+  }
+  static constexpr int NW = fit(8, EXTRA > 0) >= 2 ? 8 : 4;
+  static constexpr int NT = NW / TW;
+  static constexpr int QS = fit(NW, 2) >= 3 ? 2 : (fit(NW, 1) >= 3 || EXTRA > 0) ? 1 : 0;
+  static constexpr int S = fit(NW, QS);
+  static constexpr int kWarpExtra = QS * kQ + EXTRA;
+  static constexpr int kRing = S * kStage;
+  static constexpr int kTail = NW * kWarpExtra > kPartial ? NW * kWarpExtra : kPartial;
+  static constexpr int kSmem = NT * kRing + kTail;
+  static_assert(S >= 2 && kRing >= kPartial && kSmem + static_bytes(NW, S) <= 227 * 1024,
+                "decode stages");
 };
 
-// The loading side of a warp: walks its range and keeps the ring filled.
-// `look` finds the next block and starts the load of its page ids; `issue`,
-// one block later, uses them to start the copies of its rows.
-template <typename T, int D, int KB, int S, typename Swizzle>
+// How a block of KB rows lies in shared memory: panels of PB bytes of every row,
+// one behind the other, with the 16-byte chunks of a row swapped by its number as
+// TMA's 128-byte (64-byte) swizzle does, so that eight rows' equal chunks fall
+// into different banks.
+template <int ROW_BYTES, int KB>
+struct Tile {
+  static constexpr int PB = ROW_BYTES % 128 == 0 ? 128 : 64;
+  static constexpr int CPP = PB / 16;
+  static __device__ __forceinline__ int at(int r, int ch) {
+    const int panel = ch / CPP, c = ch % CPP;
+    return panel * (KB * PB) + r * PB + ((c ^ (PB == 128 ? r & 7 : (r >> 1) & 3)) << 4);
+  }
+};
+
+struct DecodeMaps {
+  CUtensorMap k, v;
+  int axis[3];   // what the maps' axes 1 to 3 are: 0 head, 1 token, 2 page
+};
+
+// One panel of KB tokens of one head.  The map's axes are the dims, then heads,
+// tokens and pages in the order of their strides.
+__device__ __forceinline__ void tma_load_panel(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                               int x, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+constexpr long long kWaitNs = 2000000000LL;
+
+// The loading side of a team: walks its range and keeps the ring filled.
+// `look` finds the next block and starts the load of its page id (or ids);
+// `issue`, one block later, uses them to start the copies.  All warps of the team
+// walk alike.  With pages of whole blocks (kTma) one lane starts TMA copies of
+// whole panels; else the lanes copy 16 bytes at a time, each warp its share.
+template <typename T, int D, typename Sh, int RW, int TW, int KB, bool kTma>
 struct Loader {
+  using Tl = Tile<D * int(sizeof(T)), KB>;
   static constexpr int VEC = 16 / int(sizeof(T));
-  static constexpr int CPR = D / VEC;              // 16-byte chunks per row
-  static constexpr int kLoads = KB * CPR / 32;     // chunks per lane, K or V
-  static_assert(KB * CPR % 32 == 0 && KB <= 16, "decode block");
+  static constexpr int CPR = D / VEC;                   // 16-byte chunks per row
+  static constexpr int kChunks = KB * CPR;              // ... and block
+  static constexpr int kLoads = (kChunks + 32 * TW - 1) / (32 * TW);
+  static constexpr uint32_t kAll = (1u << KB) - 1;
+  static_assert(KB <= 16, "decode block");
   const DecodeParams &p;
-  const int chunks, segs, lane;
+  const DecodeMaps &maps;
+  const int chunks, segs, lane, member;                 // member: warp of the team
   int left;                      // units left of the range
   int off, units, b, seg;        // units into the segment, and of it
   int blk, end;                  // next block of the part, and its end
@@ -232,14 +304,17 @@ struct Loader {
   Span span;
   int4 desc;
   int page, tok, head, err;
-  bool inside;
+  uint32_t rows_seen;            // mask of the looked-up block's rows that the query sees
+  int parts;                     // begun so far
+  int parts_free;                // ... and how many of them hold no query place any more
 
-  __device__ __forceinline__ Loader(const DecodeParams &p, int range, int chunks)
-      : p(p), chunks(chunks), segs(p.n_kv * chunks), lane(threadIdx.x & 31), left(0), off(0),
-        units(0), b(0), seg(0), blk(0), end(0), begins(false), page(-1), tok(0), head(0), err(0),
-        inside(false) {
+  __device__ __forceinline__ Loader(const DecodeParams &p, const DecodeMaps &maps, int chunks)
+      : p(p), maps(maps), chunks(chunks), segs(p.n_kv * chunks), lane(threadIdx.x & 31),
+        member((threadIdx.x >> 5) % TW), left(0), off(0), units(0), b(0), seg(0), blk(0), end(0),
+        begins(false), page(-1), tok(0), head(0), err(0), rows_seen(0), parts(0), parts_free(0) {
+    const int team = (threadIdx.x >> 5) / TW;
     if (p.direct) {
-      const int id = blockIdx.x / p.direct, warps = p.direct * (blockDim.x >> 5);
+      const int id = blockIdx.x / p.direct, teams = p.direct * Sh::NT;
       b = id / segs;
       seg = id - b * segs;
       head = chunks == 1 ? seg : seg / chunks;
@@ -247,23 +322,23 @@ struct Loader {
       if ((len < 0 || len > p.max_pages * p.page_size) && p.error)
         atomicOr(p.error, FA_PAGED_BAD_LENGTH);
       span = span_of<KB>(p, len);
-      const int per = (span.blocks + warps - 1) / warps;
-      const int mine = range - id * warps;
-      blk = min(mine * per, span.blocks);
+      const int per = (span.blocks + teams - 1) / teams;
+      blk = min((int(blockIdx.x) * Sh::NT + team - id * teams) * per, span.blocks);
       end = min(blk + per, span.blocks);
       begins = true;
       desc.y = b;
       desc.z = seg;
       return;
     }
+    const int range = blockIdx.x * Sh::NT + team;
     Line line;
     Place at;
     if (find<KB>(p, segs, range, 0, line, at)) {
       left = line.each + (range < line.rest ? 1 : 0);
       b = at.b;
       seg = at.seg;
-      off = at.off;
       enter();
+      off = min(at.off, units - 1);
     }
   }
 
@@ -291,11 +366,15 @@ struct Loader {
       desc.z = seg;
       head = chunks == 1 ? seg : seg / chunks;
     }
-    const int j = (span.blk0 + blk) * KB + (lane % KB);
-    inside = j >= span.lo && j < span.hi;
-    if (inside) {
+    const int j0 = (span.blk0 + blk) * KB;
+    const int n_lo = max(span.lo - j0, 0), n_hi = min(span.hi - j0, KB);
+    rows_seen = n_hi > n_lo ? (kAll >> (KB - n_hi)) & ~((1u << n_lo) - 1) : 0;
+    // With whole blocks every lane wants the page of the block's first row that
+    // counts, else lane r that of row r.
+    const int j = kTma ? j0 + n_lo : j0 + lane % KB;
+    if (kTma ? rows_seen != 0 : (rows_seen >> (lane % KB)) & 1) {
       const int idx = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
-      tok = j - idx * p.page_size;
+      tok = (kTma ? j0 : j) - idx * p.page_size;
       page = p.table[desc.y * p.table_stride + idx];
     }
     desc.x = (begins ? kPartBegins : 0) | (blk == 0 ? kSegBegins : 0);
@@ -306,39 +385,114 @@ struct Loader {
         off = 0;
         if (++seg == segs) {
           seg = 0;
-          if (++b < p.batch && left > 0) enter();
+          if (++b >= p.batch) left = 0;
+          if (left > 0) enter();
         }
       }
     }
   }
 
-  __device__ __forceinline__ void issue(uint32_t dst, int4 *at) {
-    if (!(desc.x & kDone)) {
-      int64_t o = -1;
-      if (inside) {
-        if (page >= 0 && page < p.num_pages)
-          o = page * p.page_stride + tok * p.token_stride + head * p.head_stride;
-        else
-          err = FA_PAGED_BAD_PAGE;
-      }
-      const uint32_t mask = __ballot_sync(kFull, o >= 0) & ((1u << KB) - 1);
-      if (lane == 0) *at = make_int4(desc.x | int(mask), desc.y, desc.z, 0);
-      const T *kc = static_cast<const T *>(p.kc), *vc = static_cast<const T *>(p.vc);
+  // The part's query rows, if the warp has a free place: the copy's bytes.
+  __device__ __forceinline__ uint32_t query_rows(const T *&q, int q_bytes_max) const {
+    if (!(desc.x & kPartBegins) || !p.q_chunks || parts - parts_free >= Sh::QS) return 0;
+    const int h0 = (chunks == 1 ? 0 : desc.z % chunks * (RW * TW)) + member * RW;
+    q = static_cast<const T *>(p.q) + desc.y * p.q_stride + int64_t(head * p.group + h0) * D;
+    return uint32_t(min(max(p.group - h0, 0) * D * int(sizeof(T)), q_bytes_max));
+  }
+
+  // `dst`: the stage; `bar`: its barrier; `at`: where the warp keeps what the
+  // block is; `q_places`: the warp's places for query rows.
+  __device__ __forceinline__ void issue(uint32_t dst, uint32_t bar, int4 *at,
+                                        uint32_t q_places) {
+    if (desc.x & kDone) {
+      if (lane == 0) *at = make_int4(kDone, 0, 0, 0);
+    } else {
+      const T *q = nullptr;
+      const uint32_t q_bytes = query_rows(q, Sh::kQ);
+      const uint32_t q_to = q_places + (parts % (Sh::QS > 0 ? Sh::QS : 1)) * Sh::kQ;
+      if (desc.x & kPartBegins) ++parts;
+      const bool fine = page >= 0 && page < p.num_pages;
+      if constexpr (kTma) {
+        const uint32_t mask = fine ? rows_seen : 0;
+        if (rows_seen != mask) err = FA_PAGED_BAD_PAGE;
+        if (lane == 0) {
+          *at = make_int4(desc.x | int(mask), desc.y, desc.z, q_bytes != 0);
+          const bool copies = mask != 0 && member == 0;
+          mbar_arrive_expect_tx(bar, (copies ? Sh::kStage : 0) + q_bytes);
+          if (copies) {
+            const auto at = [&](int axis) { return axis == 0 ? head : axis == 1 ? tok : page; };
+            const int c1 = at(maps.axis[0]), c2 = at(maps.axis[1]), c3 = at(maps.axis[2]);
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int c = i * 32 + lane, r = c / CPR, ch = c % CPR;
-        const int64_t row = __shfl_sync(kFull, o, r);
-        const uint32_t to = dst + (r * CPR + (ch ^ Swizzle::at(r))) * 16;
-        const int64_t from = (row < 0 ? 0 : row) + ch * VEC;
-        cp_async16(to, kc + from, row >= 0);
-        cp_async16(to + KB * CPR * 16, vc + from, row >= 0);
+            for (int i = 0; i < CPR / Tl::CPP; ++i) {
+              const int x = i * Tl::CPP * VEC;
+              const uint32_t to = dst + i * KB * Tl::PB;
+              tma_load_panel(to, &maps.k, bar, x, c1, c2, c3);
+              tma_load_panel(to + Sh::kBlock, &maps.v, bar, x, c1, c2, c3);
+            }
+          }
+          if (q_bytes) bulk_load(q_to, q, q_bytes, bar);
+        }
+      } else {
+        const uint32_t mask = rows_seen & __ballot_sync(kFull, fine);
+        if (rows_seen != mask) err = FA_PAGED_BAD_PAGE;
+        if (lane == 0) *at = make_int4(desc.x | int(mask), desc.y, desc.z, q_bytes != 0);
+        const int64_t row =
+            fine ? page * p.page_stride + tok * p.token_stride + head * p.head_stride : 0;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int c = (i * TW + member) * 32 + lane, r = c / CPR, ch = c % CPR;
+          const int64_t o = __shfl_sync(kFull, row, r % KB);
+          const bool take = (mask >> (r % KB)) & 1;
+          if (kChunks % (32 * TW) == 0 || c < kChunks) {
+            const int64_t from = (take ? o : 0) + ch * VEC;
+            cp_async16(dst + Tl::at(r, ch), static_cast<const T *>(p.kc) + from, take);
+            cp_async16(dst + Sh::kBlock + Tl::at(r, ch), static_cast<const T *>(p.vc) + from, take);
+          }
+        }
+        for (int i = lane; i < int(q_bytes) / 16; i += 32)
+          cp_async16(q_to + i * 16, q + i * VEC, true);
       }
-    } else if (lane == 0) {
-      *at = make_int4(kDone, 0, 0, 0);
     }
-    cp_async_commit();
+    if constexpr (!kTma) cp_async_commit();
   }
 };
+
+// Rows of a V block that do not count may hold anything (TMA brings whole
+// blocks): they become zeros, which the weight 0 then leaves as they are.
+template <int ROW_BYTES, int KB>
+__device__ __forceinline__ void clear_rows(uint8_t *v, uint32_t mask) {
+  for (int i = threadIdx.x & 31; i < KB * (ROW_BYTES / 16); i += 32) {
+    const int r = i / (ROW_BYTES / 16), ch = i % (ROW_BYTES / 16);
+    if (!((mask >> r) & 1))
+      *reinterpret_cast<uint4 *>(v + Tile<ROW_BYTES, KB>::at(r, ch)) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// Waits for a stage's copies, at most kWaitNs.  A wait that runs out sets
+// `abort`, after which no wait of the CTA takes long: the call then ends with
+// wrong results and FA_PAGED_TIMEOUT.
+__device__ __forceinline__ void wait_stage(uint32_t bar, uint32_t parity, int *abort) {
+  if (!sm103::mbar_wait(bar, parity, kWaitNs, abort)) *abort = 1;
+}
+
+// After a wait that ran out: waits, again for a limited time, for the copies that
+// may still be on the way to a ring whose next stage and parity these are.
+__device__ __noinline__ void drain(uint32_t full, int stages, int stage, uint32_t parity) {
+  const int never = 0;
+  for (int i = 0; i < stages; ++i)
+    sm103::mbar_wait(full + i * 8, i < stage ? parity : parity ^ 1, kWaitNs, &never);
+}
+
+// All warps of a team.
+template <int TW>
+__device__ __forceinline__ void team_sync() {
+  if constexpr (TW == 1) {
+    __syncwarp();
+  } else {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + int(threadIdx.x >> 5) / TW), "n"(32 * TW)
+                 : "memory");
+  }
+}
 
 // Floats of one workspace slot: o [rows][d], then the rows' maxima and sums.
 __host__ __device__ constexpr int slot_floats(int rows, int d) { return rows * (d + 4); }
@@ -358,40 +512,38 @@ __device__ __forceinline__ void write_stats(const DecodeParams &p, int b, int n,
   }
 }
 
-// The partial results of a CTA's warps: slot A of the part that does not begin
+// The partial results of a CTA's teams: slot A of the part that does not begin
 // its segment, slot B of the part that does and does not end it.
-template <int NW, int R>
+template <int NT, int R>
 struct Partials {
-  float m[2][NW][R], l[2][NW][R];
-  const float *o[2][NW];            // [R][D + PAD]
-  int id[2][NW];                    // segment (b * segs + seg), or -1
-  int ends[2][NW];                  // whether the part ends it
+  float m[2][NT][R], l[2][NT][R];
+  const float *o[2][NT];            // [R][D + PAD]
+  int id[2][NT];                    // segment (b * segs + seg), or -1
+  int ends[2][NT];                  // whether the part ends it
 };
 
-// Where a warp puts the partial result of a part: its ring when the part is
+// Where a team puts the partial result of a part: its ring when the part is
 // the last of its range (nothing is on the way behind it), else, so for a slot A
 // that more parts follow, its place in the workspace.
-template <int NW>
+template <int NT, int TW>
 __device__ __forceinline__ float *partial_at(const DecodeParams &p, int rows, bool last,
-                                             const uint8_t *ring) {
-  if (last) return reinterpret_cast<float *>(const_cast<uint8_t *>(ring));
-  return p.warp_part +
-         (int64_t(blockIdx.x) * NW + (threadIdx.x >> 5)) * slot_floats(rows, p.d);
+                                             uint8_t *ring) {
+  if (last) return reinterpret_cast<float *>(ring);
+  return p.team_part +
+         (int64_t(blockIdx.x) * NT + (threadIdx.x >> 5) / TW) * slot_floats(rows, p.d);
 }
 
-// Adds neighbouring partial results (see the top) once every warp is done.
-// Run 0 begins with warp 0's slot A, run 1 + w with warp w's slot B; a run
-// goes on with the slots A of the warps behind it.  A warp takes one row of
-// one run at a time.
-template <typename T, int D, int R, int NW, int PAD>
+// Adds neighbouring partial results (see the top) once every team is done.  A
+// run begins with team 0's slot A or any team's slot B and goes on with the
+// slots A of the teams behind it.  A warp takes one row of one run at a time.
+template <typename T, int D, int R, int NW, int NT, int PAD>
 __device__ __forceinline__ void merge_partials(const DecodeParams &p, int chunks,
-                                               const Partials<NW, R> &s, float *cta_part) {
+                                               const Partials<NT, R> &s, float *cta_part) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = min(R, p.group);
-  // Lane k < NW: the id in warp k's slot A, lane 16 + k: in its slot B.
-  const int id_of = (lane & 15) < NW ? s.id[lane >> 4][lane & 15] : -1;
+  // Lane k < NT: the id in team k's slot A, lane 16 + k: in its slot B.
+  const int id_of = (lane & 15) < NT ? s.id[lane >> 4][lane & 15] : -1;
   const uint32_t held = __ballot_sync(kFull, id_of >= 0);
-  // Runs begin at warp 0's slot A and at every slot B.
   uint32_t runs = held & 0xffff0001u;
   const int tasks = __popc(runs) * rows;
 #pragma unroll 1
@@ -404,7 +556,7 @@ __device__ __forceinline__ void merge_partials(const DecodeParams &p, int chunks
     // first that ends the segment.
     int count = 1;
     bool ends = s.ends[slot][w0];
-    while (!ends && w0 + count < NW) {
+    while (!ends && w0 + count < NT) {
       ends = s.ends[0][w0 + count];
       ++count;
     }
@@ -419,7 +571,7 @@ __device__ __forceinline__ void merge_partials(const DecodeParams &p, int chunks
     const float m = s.m[my_slot][w0 + mine][r], l = s.l[my_slot][w0 + mine][r];
     float mx = m;
 #pragma unroll
-    for (int o = 1; o < NW; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    for (int o = 1; o < NT; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
     const float f = sm103::ex2(m - (mx == -CUDART_INF_F ? 0.f : mx));
     float sum = 0.f;
     const bool whole = slot == 1 && ends;
@@ -468,20 +620,22 @@ __device__ __forceinline__ void merge_partials(const DecodeParams &p, int chunks
 
 // The sums of a cluster's CTAs, each at `cta_part` of its shared memory, to y.
 // A warp of the cluster takes one row.
-template <typename T, int D, int R, int NW, int KB>
+template <typename T, int D, int R, int NW, int NT, int KB>
 __device__ __forceinline__ void join_cluster(const DecodeParams &p, int chunks,
                                              const float *cta_part) {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   const int lane = threadIdx.x & 31, segs = p.n_kv * chunks;
   const int id = blockIdx.x / p.direct;
-  const int r = (blockIdx.x - id * p.direct) * NW + (threadIdx.x >> 5);
   const int b = id / segs, seg = id - b * segs;
-  const int h = (chunks == 1 ? 0 : seg % chunks * R) + r;
   const int blocks = span_of<KB>(p, __ldg(p.lens + b)).blocks;
-  const int per = (blocks + p.direct * NW - 1) / (p.direct * NW);
-  const int parts = (blocks + per * NW - 1) / (per * NW);   // CTAs that have blocks
-  if (parts > 1 && r < R && h < p.group) {
+  const int per = (blocks + p.direct * NT - 1) / (p.direct * NT);
+  const int parts = (blocks + per * NT - 1) / (per * NT);   // CTAs that have blocks
+  int r = (blockIdx.x - id * p.direct) * NW + (threadIdx.x >> 5);
+#pragma unroll 1
+  for (; parts > 1 && r < R; r += p.direct * NW) {
+    const int h = (chunks == 1 ? 0 : seg % chunks * R) + r;
+    if (h >= p.group) break;
     const int n = (chunks == 1 ? seg : seg / chunks) * p.group + h;
     const uint32_t at = sm103::smem_u32(cta_part);
     const auto remote = [](uint32_t addr, int rank) {
@@ -566,52 +720,67 @@ __device__ __forceinline__ float2 unpack2(uint32_t x) {
   return make_float2(to_f(h[0]), to_f(h[1]));
 }
 
-// Row r's chunk c of a block sits at chunk c ^ at(r) of the row, so that the
-// eight rows of an 8x8 matrix fall into different banks (rows are an odd
-// multiple of 64 bytes where CPR % 8 != 0).
-template <int CPR>
-struct TcSwizzle {
-  static __device__ __forceinline__ int at(int r) {
-    return CPR % 8 == 0 ? (r & 7) : ((r >> 1) & 3);
-  }
+// Rows per team and the warps that share it.
+template <int R>
+struct TcTeam {
+  static constexpr int RW = R == 8 ? 8 : 16, TW = R / RW;
 };
-
 template <int D, int R>
-using TcShape = Shape<__half, D, R, 16, 0, 2>;
+using TcShape = Shape<__half, D, TcTeam<R>::RW, TcTeam<R>::TW, 16, 0>;
 
 // S = Q K^T and O = P V by m16n8k16 products: Q's rows are the group's query
-// heads, padded to 16, and a warp takes 16 keys at a time through its own ring
-// of stages, filled by cp.async ahead of use.
+// heads, padded to 16, and a team takes 16 keys at a time through its own ring
+// of stages, filled by cp.async ahead of use.  A K block's place is filled
+// again as soon as S is computed, a V block's after O.
 //
 // P goes into the second product as the sum of two 16-bit numbers, so that
-// its rounding (2^-17 for bf16) stays below y's own.  With R = 8 the two
+// its rounding (2^-17 for bf16) stays below y's own.  With 8 rows the two
 // halves share one product: rows 0-7 hold P rounded, rows 8-15 what is left
-// of it, and the halves of the result are added at the end.  With R = 16 they
+// of it, and the halves of the result are added at the end.  With 16 rows they
 // are two products.
-template <typename T, int D, int R>
+template <typename T, int D, int R, bool kTma>
 __global__ void __launch_bounds__(TcShape<D, R>::NW * 32, 1)
-decode_tc_kernel(const __grid_constant__ DecodeParams p) {
+decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ DecodeMaps maps) {
   using Sh = TcShape<D, R>;
-  using Sw = TcSwizzle<D / 8>;
-  constexpr int KB = 16, S = Sh::S, NW = Sh::NW;
-  constexpr int CPR = D / 8;
-  constexpr int NR = R / 8;         // rows of a lane
+  using Tl = Tile<D * 2, 16>;
+  constexpr int RW = TcTeam<R>::RW, TW = TcTeam<R>::TW;
+  constexpr int KB = 16, S = Sh::S, NW = Sh::NW, NT = Sh::NT;
+  constexpr int NR = RW / 8;        // rows of a lane
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ Partials<NW, R> s_part;
+  __shared__ Partials<NT, R> s_part;
   __shared__ int4 s_desc[NW][S];
+  __shared__ uint64_t s_full[NT][S];
+  __shared__ int s_abort;
   asm volatile("griddepcontrol.launch_dependents;");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint8_t *my = smem + warp * S * Sh::kStage;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / TW;
+  const int row0 = warp % TW * RW;  // first row of the team's that is the warp's
+  uint8_t *my = smem + team * Sh::kRing;
   const uint32_t ring = sm103::smem_u32(my);
+  const uint32_t q_places = sm103::smem_u32(smem) + NT * Sh::kRing + warp * Sh::kWarpExtra;
+  const uint32_t full = sm103::smem_u32(&s_full[team][0]);
   const T *q = static_cast<const T *>(p.q);
   const int chunks = (p.group + R - 1) / R, segs = p.n_kv * chunks;
-  if (lane < 2) s_part.id[lane][warp] = -1;
+  if (lane < 2) {
+    s_part.id[lane][team] = -1;
+    s_part.ends[lane][team] = 1;
+    s_part.o[lane][team] = reinterpret_cast<const float *>(my);
+  }
+  if constexpr (kTma) {
+    if (threadIdx.x == 0) {
+      sm103::tma_prefetch_map(&maps.k);
+      sm103::tma_prefetch_map(&maps.v);
+      s_abort = 0;
+      for (int i = 0; i < NT * S; ++i) sm103::mbar_init(sm103::smem_u32(&s_full[0][0] + i), TW);
+      sm103::mbar_fence_init();
+    }
+    __syncthreads();
+  }
 
-  Loader<T, D, KB, S, Sw> load(p, blockIdx.x * NW + warp, chunks);
+  Loader<T, D, Sh, RW, TW, KB, kTma> load(p, maps, chunks);
   load.look();
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) {
-    load.issue(ring + i * Sh::kStage, &s_desc[warp][i]);
+    load.issue(ring + i * Sh::kStage, full + i * 8, &s_desc[warp][i], q_places);
     load.look();
   }
 
@@ -620,6 +789,7 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p) {
   const int k_row = (lane & 7) + ((lane >> 4) << 3), k_ch = (lane >> 3) & 1;
   const int v_row = (lane & 7) + (((lane >> 3) & 1) << 3), v_ch = lane >> 4;
   int stage = 0, fill = S - 1, heads = 0, n0 = 0;
+  uint32_t parity = 0;
   uint32_t qa[D / 16][2 * NR];
   float o[D / 8][4];
   float m[NR], l[NR];
@@ -627,39 +797,56 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p) {
 
 #pragma unroll 1
   while (true) {
-    cp_async_wait<S - 2>();
-    __syncwarp();
+    if constexpr (!kTma) cp_async_wait<S - 2>();
+    team_sync<TW>();                // the stage to fill has been read
     const int4 desc = s_desc[warp][stage];
     if (desc.x & kDone) break;
+    if constexpr (kTma) wait_stage(full + stage * 8, parity, &s_abort);
     const uint32_t kb = ring + stage * Sh::kStage, vb = kb + Sh::kBlock;
-    load.issue(ring + fill * Sh::kStage, &s_desc[warp][fill]);
-    load.look();
-    fill = fill + 1 == S ? 0 : fill + 1;
-    stage = stage + 1 == S ? 0 : stage + 1;
 
     if (desc.x & kPartBegins) {
-      const int hk = desc.z / chunks, h0 = (desc.z - hk * chunks) * R;
-      heads = min(R, p.group - h0);
-      n0 = hk * p.group + h0;
       opens = desc.x & kSegBegins;
-      const T *qr = q + desc.y * p.q_stride + int64_t(n0) * D;
-      // Fragment i of a step: rows row (and row + 8 for odd i with R = 16).  Rows
-      // behind the last head repeat it; nothing reads their results.
+      const int hk = chunks == 1 ? desc.z : desc.z / chunks;
+      const int h0 = (chunks == 1 ? 0 : (desc.z - hk * chunks) * R) + row0;
+      heads = min(RW, p.group - h0);           // may be negative
+      n0 = hk * p.group + h0;
+      if (desc.w) {
+        // Fragments by ldmatrix: rows behind the last head hold anything, and
+        // nothing reads their results.
+        const uint32_t qs = q_places + load.parts_free % (Sh::QS > 0 ? Sh::QS : 1) * Sh::kQ;
+        const int q_row = NR == 1 ? (lane & 7) : (lane & 7) + (((lane >> 3) & 1) << 3);
 #pragma unroll
-      for (int i = 0; i < 2 * NR; ++i) {
-        const int r = min(row + (NR == 2 ? (i & 1) * 8 : 0), heads - 1);
-        const T *src = qr + r * D + col + (NR == 2 ? i >> 1 : i) * 8;
-        if (p.q_pairs) {
+        for (int ks = 0; ks < D / 16; ks += NR == 1 ? 2 : 1) {
+          uint32_t x[4];
+          const int ch = ks * 2 + (NR == 1 ? lane >> 3 : lane >> 4);
+          ldsm4(x, qs + q_row * (D * 2) + ch * 16);
+          if constexpr (NR == 1) {
+            qa[ks][0] = x[0];
+            qa[ks][1] = x[1];
+            qa[ks + 1][0] = x[2];
+            qa[ks + 1][1] = x[3];
+          } else {
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            qa[ks][i] = __ldg(reinterpret_cast<const uint32_t *>(src + ks * 16));
-        } else {
-          const uint16_t *h = reinterpret_cast<const uint16_t *>(src);
+            for (int i = 0; i < 4; ++i) qa[ks][i] = x[i];
+          }
+        }
+        __syncwarp();               // the place is free
+      } else {
+        // Rows behind the last head repeat it.
+        const T *qr = q + desc.y * p.q_stride + int64_t(n0 - row0) * D;
+#pragma unroll
+        for (int i = 0; i < 2 * NR; ++i) {
+          // Fragment i of a step: rows row (and row + 8 for odd i with 16).
+          const int r = min(row0 + row + (NR == 2 ? (i & 1) * 8 : 0),
+                            max(heads + row0, 1) - 1);
+          const uint16_t *h = reinterpret_cast<const uint16_t *>(
+              qr + r * D + col + (NR == 2 ? i >> 1 : i) * 8);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
             qa[ks][i] = uint32_t(h[ks * 16]) | uint32_t(h[ks * 16 + 1]) << 16;
         }
       }
+      ++load.parts_free;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
 #pragma unroll
@@ -670,6 +857,18 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p) {
         l[i] = 0.f;
       }
     }
+    load.issue(ring + fill * Sh::kStage, full + fill * 8, &s_desc[warp][fill], q_places);
+    load.look();
+    fill = fill + 1 == S ? 0 : fill + 1;
+    if (++stage == S) {
+      stage = 0;
+      parity ^= 1;
+    }
+    const uint32_t mask = desc.x & 0xffff;
+    if (kTma && mask != 0xffff) {
+      clear_rows<D * 2, KB>(my + (vb - ring), mask);
+      team_sync<TW>();
+    }
 
     float sa[2][2][4];              // [chain][key half][fragment]
 #pragma unroll
@@ -677,9 +876,9 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p) {
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       uint32_t kf[4];
-      ldsm4(kf, kb + (k_row * CPR + ((ks * 2 + k_ch) ^ Sw::at(k_row))) * 16);
+      ldsm4(kf, kb + Tl::at(k_row, ks * 2 + k_ch));
       uint32_t a[4];
-      if constexpr (R == 8) {
+      if constexpr (NR == 1) {
         a[0] = qa[ks][0];
         a[1] = 0;
         a[2] = qa[ks][1];
@@ -718,7 +917,7 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p) {
         l[i] *= f;
 #pragma unroll
         for (int k = 0; k < D / 8; ++k) {
-          if constexpr (R == 8) {
+          if constexpr (NR == 1) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[k][e] *= f;
           } else {
@@ -745,8 +944,8 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p) {
 #pragma unroll
     for (int dt = 0; dt < D / 16; ++dt) {
       uint32_t vf[4];
-      ldsm4_t(vf, vb + (v_row * CPR + ((dt * 2 + v_ch) ^ Sw::at(v_row))) * 16);
-      if constexpr (R == 8) {
+      ldsm4_t(vf, vb + Tl::at(v_row, dt * 2 + v_ch));
+      if constexpr (NR == 1) {
         const uint32_t a[4] = {hi[0][0], lo[0][0], hi[0][1], lo[0][1]};
         mma16816<T>(o[2 * dt], a, vf[0], vf[1]);
         mma16816<T>(o[2 * dt + 1], a, vf[2], vf[3]);
@@ -759,6 +958,8 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p) {
         mma16816<T>(o[2 * dt + 1], c, vf[2], vf[3]);
       }
     }
+
+    if (kTma && mask != 0xffff) sm103::fence_proxy_async_smem();   // before the next copy there
 
     if (desc.x & kPartEnds) {
       const bool ends = desc.x & kSegEnds;
@@ -777,8 +978,8 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p) {
           T *y = static_cast<T *>(p.y) + desc.y * p.y_stride + int64_t(n0 + r) * D + col;
 #pragma unroll
           for (int k = 0; k < D / 8; ++k) {
-            const float x0 = (R == 8 ? o[k][0] + o[k][2] : o[k][i * 2]) * inv;
-            const float x1 = (R == 8 ? o[k][1] + o[k][3] : o[k][i * 2 + 1]) * inv;
+            const float x0 = (NR == 1 ? o[k][0] + o[k][2] : o[k][i * 2]) * inv;
+            const float x1 = (NR == 1 ? o[k][1] + o[k][3] : o[k][i * 2 + 1]) * inv;
             if (p.y_pairs) {
               *reinterpret_cast<uint32_t *>(y + k * 8) = pack2<T>(x0, x1);
             } else {
@@ -789,105 +990,138 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p) {
           if ((lane & 3) == 0) write_stats(p, desc.y, n0 + r, m[i] * kLn2, l[i]);
         }
       } else {
-        __syncwarp();                // the ring has been read
+        team_sync<TW>();            // the ring has been read
         const int slot = opens ? 1 : 0;
-        float *dst = partial_at<NW>(p, R, desc.x & kRangeEnds, my);
+        float *dst = partial_at<NT, TW>(p, R, desc.x & kRangeEnds, my);
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
-          const int r = row + i * 8;
+          const int r = row0 + row + i * 8;
           if ((lane & 3) == 0) {
-            s_part.m[slot][warp][r] = m[i];
-            s_part.l[slot][warp][r] = l[i];
+            s_part.m[slot][team][r] = m[i];
+            s_part.l[slot][team][r] = l[i];
           }
 #pragma unroll
           for (int k = 0; k < D / 8; ++k)
             *reinterpret_cast<float2 *>(dst + r * (D + Sh::PAD) + col + k * 8) =
-                R == 8 ? make_float2(o[k][0] + o[k][2], o[k][1] + o[k][3])
+                NR == 1 ? make_float2(o[k][0] + o[k][2], o[k][1] + o[k][3])
                        : make_float2(o[k][i * 2], o[k][i * 2 + 1]);
         }
         if (lane == 0) {
-          s_part.id[slot][warp] = id;
-          s_part.ends[slot][warp] = ends;
-          s_part.o[slot][warp] = dst;
+          s_part.id[slot][team] = id;
+          s_part.ends[slot][team] = ends;
+          s_part.o[slot][team] = dst;
         }
       }
     }
   }
   __syncthreads();
-  float *cta_part = reinterpret_cast<float *>(smem + NW * (S * Sh::kStage + Sh::kExtra));
-  merge_partials<T, D, R, NW, Sh::PAD>(p, chunks, s_part, cta_part);
-  if (p.direct > 1) join_cluster<T, D, R, NW, KB>(p, chunks, cta_part);
+  float *cta_part = reinterpret_cast<float *>(smem + NT * Sh::kRing);
+  merge_partials<T, D, R, NW, NT, Sh::PAD>(p, chunks, s_part, cta_part);
+  if (p.direct > 1) join_cluster<T, D, R, NW, NT, KB>(p, chunks, cta_part);
+  if constexpr (kTma) {
+    if (s_abort) {
+      load.err |= FA_PAGED_TIMEOUT;
+      drain(full, S, stage, parity);
+    }
+  }
   if (load.err && p.error) atomicOr(p.error, load.err);
 }
 
 // ---------------------------------------------------------------------------
 // fp32 kernel, on the CUDA cores
 // ---------------------------------------------------------------------------
-// Row r's chunk c at chunk c ^ at(r): the eight lanes of a 128-byte shared
-// memory access read two rows' four neighbouring chunks.
-struct SimtSwizzle {
-  static __device__ __forceinline__ int at(int r) { return (r & 1) << 2; }
-};
-
 template <int D, int R>
-using SimtShape = Shape<float, D, R, 8, (R * D + 8 * R) * 4, 2>;
+using SimtShape = Shape<float, D, R, 1, 8, 8 * R * 4>;
 
 // A warp takes 8 keys at a time.  Scores: four lanes per key, each a quarter
 // of the dims (every fourth chunk).  Output: each lane D / 32 dims of all R heads.
-template <int D, int R>
+template <int D, int R, bool kTma>
 __global__ void __launch_bounds__(SimtShape<D, R>::NW * 32, 1)
-decode_simt_kernel(const __grid_constant__ DecodeParams p) {
+decode_simt_kernel(const __grid_constant__ DecodeParams p,
+                   const __grid_constant__ DecodeMaps maps) {
   using Sh = SimtShape<D, R>;
   constexpr int KB = 8, S = Sh::S, NW = Sh::NW;
+  using Tl = Tile<D * 4, KB>;
   constexpr int CPR = D / 4;
   constexpr int VW = D % 128 == 0 ? 4 : D % 64 == 0 ? 2 : 1;   // dims per access
   constexpr int NV = D / (32 * VW);                             // accesses per row
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Partials<NW, R> s_part;
   __shared__ int4 s_desc[NW][S];
+  __shared__ uint64_t s_full[NW][S];
+  __shared__ int s_abort;
   asm volatile("griddepcontrol.launch_dependents;");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float *s_q = reinterpret_cast<float *>(smem + NW * S * Sh::kStage) + warp * (R * D + 8 * R);
-  float *s_p = s_q + R * D;         // q [R][D], weights [8][R]
-  const uint8_t *my = smem + warp * S * Sh::kStage;
-  const uint32_t ring = sm103::smem_u32(my);
+  uint8_t *my = smem + warp * Sh::kRing;
+  uint8_t *extra = smem + NW * Sh::kRing + warp * Sh::kWarpExtra;
+  const uint32_t ring = sm103::smem_u32(my), q_places = sm103::smem_u32(extra);
+  float *s_p = reinterpret_cast<float *>(extra + Sh::QS * Sh::kQ);   // weights [8][R]
+  float *s_q = nullptr;                                               // the part's query rows
   const int chunks = (p.group + R - 1) / R, segs = p.n_kv * chunks;
-  if (lane < 2) s_part.id[lane][warp] = -1;
+  if (lane < 2) {
+    s_part.id[lane][warp] = -1;
+    s_part.ends[lane][warp] = 1;
+    s_part.o[lane][warp] = reinterpret_cast<const float *>(my);
+  }
 
-  Loader<float, D, KB, S, SimtSwizzle> load(p, blockIdx.x * NW + warp, chunks);
+  const uint32_t full = sm103::smem_u32(&s_full[warp][0]);
+  if constexpr (kTma) {
+    if (threadIdx.x == 0) {
+      sm103::tma_prefetch_map(&maps.k);
+      sm103::tma_prefetch_map(&maps.v);
+      s_abort = 0;
+      for (int i = 0; i < NW * S; ++i) sm103::mbar_init(sm103::smem_u32(&s_full[0][0] + i), 1);
+      sm103::mbar_fence_init();
+    }
+    __syncthreads();
+  }
+
+  Loader<float, D, Sh, R, 1, KB, kTma> load(p, maps, chunks);
   load.look();
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) {
-    load.issue(ring + i * Sh::kStage, &s_desc[warp][i]);
+    load.issue(ring + i * Sh::kStage, full + i * 8, &s_desc[warp][i], q_places);
     load.look();
   }
 
   const int key = lane >> 2, quarter = lane & 3;
   int stage = 0, fill = S - 1, heads = 0, n0 = 0;
+  uint32_t parity = 0;
   float o[R][NV * VW], m[R], l[R];
   bool opens = false;
 
 #pragma unroll 1
   while (true) {
-    cp_async_wait<S - 2>();
-    __syncwarp();
+    if constexpr (!kTma) cp_async_wait<S - 2>();
+    __syncwarp();                    // the stage to fill has been read
     const int4 desc = s_desc[warp][stage];
     if (desc.x & kDone) break;
-    const float *kb = reinterpret_cast<const float *>(my + stage * Sh::kStage);
-    const float *vb = kb + KB * D;
-    load.issue(ring + fill * Sh::kStage, &s_desc[warp][fill]);
+    if constexpr (kTma) wait_stage(full + stage * 8, parity, &s_abort);
+    uint8_t *kb = my + stage * Sh::kStage, *vb = kb + Sh::kBlock;
+    load.issue(ring + fill * Sh::kStage, full + fill * 8, &s_desc[warp][fill], q_places);
     load.look();
     fill = fill + 1 == S ? 0 : fill + 1;
-    stage = stage + 1 == S ? 0 : stage + 1;
+    if (++stage == S) {
+      stage = 0;
+      parity ^= 1;
+    }
+    const uint32_t mask = desc.x & 0xff;
+    if (kTma && mask != 0xff) clear_rows<D * 4, KB>(vb, mask);
 
     if (desc.x & kPartBegins) {
-      const int hk = desc.z / chunks, h0 = (desc.z - hk * chunks) * R;
+      opens = desc.x & kSegBegins;
+      const int hk = chunks == 1 ? desc.z : desc.z / chunks;
+      const int h0 = chunks == 1 ? 0 : (desc.z - hk * chunks) * R;
       heads = min(R, p.group - h0);
       n0 = hk * p.group + h0;
-      opens = desc.x & kSegBegins;
-      const float *qr = static_cast<const float *>(p.q) + desc.y * p.q_stride + int64_t(n0) * D;
-      for (int i = lane; i < R * D; i += 32) s_q[i] = i < heads * D ? __ldg(qr + i) : 0.f;
-      __syncwarp();
+      // A part keeps its place until it ends.
+      s_q = reinterpret_cast<float *>(extra + load.parts_free % Sh::QS * Sh::kQ);
+      if (!desc.w) {
+        const float *qr = static_cast<const float *>(p.q) + desc.y * p.q_stride + int64_t(n0) * D;
+        for (int i = lane; i < heads * D; i += 32) s_q[i] = __ldg(qr + i);
+        if (kTma) sm103::fence_proxy_async_smem();   // before a later copy to this place
+        __syncwarp();
+      }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         m[r] = -CUDART_INF_F;
@@ -902,9 +1136,9 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p) {
     for (int r = 0; r < R; ++r) s[r] = 0.f;
 #pragma unroll
     for (int i = 0; i < CPR / 4; ++i) {
-      const int c = i * 4 + quarter;
-      const float4 kv =
-          *reinterpret_cast<const float4 *>(kb + (key * CPR + (c ^ SimtSwizzle::at(key))) * 4);
+      // Odd keys take the other half of a panel, for the banks' sake.
+      const int c = (i * 4 + quarter) ^ ((key & 1) << 2);
+      const float4 kv = *reinterpret_cast<const float4 *>(kb + Tl::at(key, c));
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const float4 qv = *reinterpret_cast<const float4 *>(s_q + r * D + c * 4);
@@ -947,7 +1181,7 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int d = (i * 32 + lane) * VW;
-        const float *src = vb + (k * CPR + ((d >> 2) ^ SimtSwizzle::at(k))) * 4 + (d & 3);
+        const float *src = reinterpret_cast<const float *>(vb + Tl::at(k, d >> 2)) + (d & 3);
         float v[VW];
         if constexpr (VW == 4) {
           const float4 x = *reinterpret_cast<const float4 *>(src);
@@ -965,7 +1199,10 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p) {
       }
     }
 
+    if (kTma && mask != 0xff) sm103::fence_proxy_async_smem();   // before the next copy there
+
     if (desc.x & kPartEnds) {
+      ++load.parts_free;
       const bool ends = desc.x & kSegEnds;
       const int id = desc.y * segs + desc.z;
 #pragma unroll
@@ -975,8 +1212,8 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p) {
       }
       const bool whole = opens && ends;
       const int slot = opens ? 1 : 0;
-      float *dst = partial_at<NW>(p, R, desc.x & kRangeEnds, my);
       __syncwarp();                  // the ring has been read
+      float *dst = partial_at<NW, 1>(p, R, desc.x & kRangeEnds, my);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (r >= heads) continue;
@@ -1004,9 +1241,15 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p) {
     }
   }
   __syncthreads();
-  float *cta_part = reinterpret_cast<float *>(smem + NW * (S * Sh::kStage + Sh::kExtra));
-  merge_partials<float, D, R, NW, Sh::PAD>(p, chunks, s_part, cta_part);
-  if (p.direct > 1) join_cluster<float, D, R, NW, KB>(p, chunks, cta_part);
+  float *cta_part = reinterpret_cast<float *>(smem + NW * Sh::kRing);
+  merge_partials<float, D, R, NW, NW, Sh::PAD>(p, chunks, s_part, cta_part);
+  if (p.direct > 1) join_cluster<float, D, R, NW, NW, KB>(p, chunks, cta_part);
+  if constexpr (kTma) {
+    if (s_abort) {
+      load.err |= FA_PAGED_TIMEOUT;
+      drain(full, S, stage, parity);
+    }
+  }
   if (load.err && p.error) atomicOr(p.error, load.err);
 }
 
@@ -1020,7 +1263,7 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p) {
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
 
-template <typename T, int D, int KB, int NW>
+template <typename T, int D, int KB, int NT>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(
     const __grid_constant__ DecodeParams p, int rows, int by_segment) {
   constexpr int PL = D / 32;
@@ -1030,20 +1273,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y;
   const int chunks = (p.group + rows - 1) / rows, segs = p.n_kv * chunks;
   Line line;
-  Place at;
+  Place at{0, 0, 0, 1};
   int first_unit;                    // of the segment
   if (by_segment) {
     at.b = blockIdx.x / segs;
     at.seg = blockIdx.x - at.b * segs;
     first_unit = segment_start<KB>(p, segs, at, line);
   } else {
-    const int behind = (blockIdx.x + 1) * NW;
+    const int behind = (blockIdx.x + 1) * NT;
     find<KB>(p, segs, behind, 1, line, at);
     first_unit = line.start(behind) - 1 - at.off;
   }
   // The CTAs of its first and last block.
-  const int i = line.range_of(first_unit + (kSwitchBlocks >> p.unit_shift)) / NW;
-  const int last = line.range_of(first_unit + at.units - 1) / NW;
+  const int i = line.range_of(first_unit + (kSwitchBlocks >> p.unit_shift)) / NT;
+  const int last = min(line.range_of(first_unit + at.units - 1) / NT, p.grid - 1);
   const int h = (chunks == 1 ? 0 : at.seg % chunks * rows) + r;
   const int n = (chunks == 1 ? at.seg : at.seg / chunks) * p.group + h;
 
@@ -1104,13 +1347,89 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(
   if (d == 0) write_stats(p, at.b, n, top * kLn2, total);
 }
 
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn decode_encode_fn() {
+  static const EncodeFn fn = [] {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<EncodeFn>(ptr);
+  }();
+  return fn;
+}
+
+// The cache as a 4-D tensor.  False: a block of KB keys may leave its page, or the
+// strides are not those of nested axes, as TMA wants them.
+template <typename T, int D, int KB>
+bool make_page_maps(DecodeMaps &maps, const DecodeParams &p) {
+  using Tl = Tile<D * int(sizeof(T)), KB>;
+  const EncodeFn enc = decode_encode_fn();
+  if (enc == nullptr || p.page_size % KB != 0) return false;
+  const int64_t count[3] = {p.n_kv, p.page_size, p.num_pages};
+  const int64_t stride[3] = {p.head_stride, p.token_stride, p.page_stride};
+  // By stride, axes of one entry (whose stride is 0 here) last.
+  int order[3] = {0, 1, 2};
+  const auto later = [&](int a, int b) {
+    if ((count[a] == 1) != (count[b] == 1)) return count[a] == 1;
+    return stride[a] > stride[b];
+  };
+  for (int i = 0; i < 2; ++i)
+    for (int k = 0; k < 2 - i; ++k)
+      if (later(order[k], order[k + 1])) {
+        const int t = order[k];
+        order[k] = order[k + 1];
+        order[k + 1] = t;
+      }
+  cuuint64_t dims[4] = {D}, strides[3];
+  cuuint32_t box[4] = {Tl::PB / sizeof(T), 1, 1, 1};
+  int64_t inner = 1, extent = D;   // stride and extent of the axis before, in elements
+  for (int i = 0; i < 3; ++i) {
+    const int a = order[i];
+    const int64_t own = count[a] == 1 ? extent : stride[a];
+    if (own < extent || (i > 0 && own % inner != 0) ||
+        own * int64_t(sizeof(T)) >= (int64_t(1) << 40) || count[a] > (int64_t(1) << 31))
+      return false;
+    inner = own;
+    extent = own * count[a];
+    dims[i + 1] = cuuint64_t(count[a]);
+    strides[i] = cuuint64_t(own) * sizeof(T);
+    if (strides[i] % 16 != 0) return false;
+    if (a == 1) box[i + 1] = KB;
+    maps.axis[i] = a;
+  }
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  const CUtensorMapDataType type = std::is_same<T, float>::value    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto encode = [&](CUtensorMap *map, const void *base) {
+    return enc(map, type, 4, const_cast<void *>(base), dims, strides, box, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE,
+               Tl::PB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  return encode(&maps.k, p.kc) && encode(&maps.v, p.vc);
+}
+
 // The main kernel and the join, which is launched as its dependent so that its
 // launch overlaps the main kernel's run.
-template <typename T, int D, int R, int KB, int NW, typename Kernel>
-cudaError_t launch_both(DecodeParams p, Kernel kernel, int smem, int sms, cudaStream_t s) {
+template <typename T, int D, typename Sh, int KB, typename Kernel>
+cudaError_t launch_shape(DecodeParams p, Kernel with_tma, Kernel without, int sms,
+                         cudaStream_t s) {
+  constexpr int R = Sh::R, NW = Sh::NW, NT = Sh::NT;
   const int64_t segments = int64_t(p.batch) * p.n_kv * ((p.group + R - 1) / R);
+  DecodeMaps maps;
+  const bool tma = make_page_maps<T, D, KB>(maps, p);
+  const Kernel kernel = tma ? with_tma : without;
   cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr{};
@@ -1120,108 +1439,68 @@ cudaError_t launch_both(DecodeParams p, Kernel kernel, int smem, int sms, cudaSt
   if (p.direct) {
     cfg.gridDim = dim3(unsigned(segments) * p.direct);
     cfg.blockDim = dim3(NW * 32);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = Sh::kSmem;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = p.direct;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return cudaLaunchKernelEx(&cfg, kernel, p, maps);
   }
   p.grid = sms;
-  p.ranges = sms * NW;
+  p.ranges = sms * NT;
   const int64_t blocks = (int64_t(p.max_pages) * p.page_size + KB - 1) / KB + 1 + kSwitchBlocks;
   p.unit_shift = 0;
   while (segments * ((blocks >> p.unit_shift) + 1) >= (int64_t(1) << 31)) ++p.unit_shift;
-  kernel<<<p.grid, NW * 32, smem, s>>>(p);
+  kernel<<<p.grid, NW * 32, Sh::kSmem, s>>>(p, maps);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int by_segment = segments <= p.grid;
   cfg.gridDim = dim3(unsigned(by_segment ? segments : p.grid), unsigned(p.group < R ? p.group : R));
   cfg.blockDim = dim3(kJoinWarps * 32);
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<T, D, KB, NW>, p, R, by_segment);
-}
-
-template <int D, int R>
-cudaError_t launch_simt(const DecodeParams &p, int sms, cudaStream_t s) {
-  using Sh = SimtShape<D, R>;
-  return launch_both<float, D, R, 8, Sh::NW>(p, decode_simt_kernel<D, R>, Sh::kSmem, sms, s);
+  return cudaLaunchKernelEx(&cfg, join_kernel<T, D, KB, NT>, p, R, by_segment);
 }
 
 template <typename T, int D, int R>
+cudaError_t launch_tc_rows(const DecodeParams &p, int sms, cudaStream_t s) {
+  return launch_shape<T, D, TcShape<D, R>, 16>(p, decode_tc_kernel<T, D, R, true>,
+                                               decode_tc_kernel<T, D, R, false>, sms, s);
+}
+
+template <typename T, int D>
 cudaError_t launch_tc(const DecodeParams &p, int sms, cudaStream_t s) {
-  using Sh = TcShape<D, R>;
-  return launch_both<T, D, R, 16, Sh::NW>(p, decode_tc_kernel<T, D, R>, Sh::kSmem, sms, s);
+  switch (p.rows) {
+    case 8: return launch_tc_rows<T, D, 8>(p, sms, s);
+    case 16: return launch_tc_rows<T, D, 16>(p, sms, s);
+    case 32: return launch_tc_rows<T, D, 32>(p, sms, s);
+    default: return launch_tc_rows<T, D, 64>(p, sms, s);
+  }
+}
+
+template <int D, int R>
+cudaError_t launch_simt_rows(const DecodeParams &p, int sms, cudaStream_t s) {
+  return launch_shape<float, D, SimtShape<D, R>, 8>(p, decode_simt_kernel<D, R, true>,
+                                                    decode_simt_kernel<D, R, false>, sms, s);
 }
 
 template <int D>
-cudaError_t launch_d(const DecodeParams &p, fa_dtype dt, int rows, int sms, cudaStream_t s) {
-  if (dt == FA_DTYPE_FP32) {
-    switch (rows) {
-      case 1: return launch_simt<D, 1>(p, sms, s);
-      case 2: return launch_simt<D, 2>(p, sms, s);
-      case 4: return launch_simt<D, 4>(p, sms, s);
-      default: return launch_simt<D, 8>(p, sms, s);
-    }
-  }
-  if (dt == FA_DTYPE_FP16)
-    return rows == 8 ? launch_tc<__half, D, 8>(p, sms, s) : launch_tc<__half, D, 16>(p, sms, s);
-  return rows == 8 ? launch_tc<__nv_bfloat16, D, 8>(p, sms, s)
-                   : launch_tc<__nv_bfloat16, D, 16>(p, sms, s);
-}
-
-template <int D>
-int warps_of_d(bool tc, int rows) {
-  if (tc) return rows == 8 ? TcShape<D, 8>::NW : TcShape<D, 16>::NW;
-  return rows == 1 ? SimtShape<D, 1>::NW : rows == 2 ? SimtShape<D, 2>::NW
-         : rows == 4 ? SimtShape<D, 4>::NW : SimtShape<D, 8>::NW;
-}
-
-int warps_of(bool tc, int rows, int d) {
-  switch (d) {
-    case 32: return warps_of_d<32>(tc, rows);
-    case 64: return warps_of_d<64>(tc, rows);
-    case 96: return warps_of_d<96>(tc, rows);
-    case 128: return warps_of_d<128>(tc, rows);
-    default: return warps_of_d<192>(tc, rows);
+cudaError_t launch_simt(const DecodeParams &p, int sms, cudaStream_t s) {
+  switch (p.rows) {
+    case 1: return launch_simt_rows<D, 1>(p, sms, s);
+    case 2: return launch_simt_rows<D, 2>(p, sms, s);
+    case 4: return launch_simt_rows<D, 4>(p, sms, s);
+    default: return launch_simt_rows<D, 8>(p, sms, s);
   }
 }
+
+#define FAV_DECODE_BY_DIM(FN, ...)            \
+  switch (p.d) {                              \
+    case 32: return FN<__VA_ARGS__ 32>(p, sms, s);   \
+    case 64: return FN<__VA_ARGS__ 64>(p, sms, s);   \
+    case 96: return FN<__VA_ARGS__ 96>(p, sms, s);   \
+    case 128: return FN<__VA_ARGS__ 128>(p, sms, s); \
+    case 192: return FN<__VA_ARGS__ 192>(p, sms, s); \
+  }                                           \
+  return cudaErrorInvalidValue
 
 }  // namespace
-
-// The shape of a call, from its scalars alone.
-DecodePlan decode_plan(fa_dtype dt, int batch, int n_kv, int group, int d, int64_t max_keys,
-                       int sms) {
-  DecodePlan plan;
-  // fp32: the heads whose outputs a lane's registers hold at once.  16-bit types:
-  // the rows of one product, all 16 of which serve P rounded once a group has
-  // more than 8 heads.
-  const bool tc = dt != FA_DTYPE_FP32;
-  plan.rows = tc ? (group <= 8 ? 8 : 16) : group <= 1 ? 1 : group <= 2 ? 2 : group <= 4 ? 4 : 8;
-  plan.warps = warps_of(tc, plan.rows, d);
-  // The largest cluster per segment that still puts all of them on the GPU at
-  // once, if its warps get at most kDirectBlocks blocks each.
-  const int kb = tc ? 16 : 8;
-  const int64_t blocks = (max_keys + kb - 1) / kb + 1;
-  const int64_t segments = int64_t(batch) * n_kv * ((group + plan.rows - 1) / plan.rows);
-  int ctas = 1;
-  while (ctas < kMaxDirect && segments * ctas * 2 <= sms && ctas * plan.warps < blocks) ctas *= 2;
-  plan.direct =
-      segments * ctas <= sms && blocks <= int64_t(ctas) * plan.warps * kDirectBlocks ? ctas : 0;
-  return plan;
-}
-
-size_t decode_part_floats(int rows, int d) { return size_t(slot_floats(rows, d)); }
-
-cudaError_t launch_paged_decode(const DecodeParams &p, fa_dtype dt, int sms, cudaStream_t s) {
-  const int rows = p.rows;
-  switch (p.d) {
-    case 32: return launch_d<32>(p, dt, rows, sms, s);
-    case 64: return launch_d<64>(p, dt, rows, sms, s);
-    case 96: return launch_d<96>(p, dt, rows, sms, s);
-    case 128: return launch_d<128>(p, dt, rows, sms, s);
-    case 192: return launch_d<192>(p, dt, rows, sms, s);
-  }
-  return cudaErrorInvalidValue;
-}
-
 }  // namespace fav
