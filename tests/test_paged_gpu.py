@@ -218,7 +218,8 @@ RAGGED = [1, 0, 17, 16, 15, 130, 64, 3, 999, 0, 33]
 @pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
 @pytest.mark.parametrize("dim", [32, 64, 96, 128, 192])
 @pytest.mark.parametrize("heads,heads_kv,page,layout", [
-    (2, 2, 16, "NHD"), (8, 2, 24, "HND"), (5, 5, 1, "NHD"), (7, 1, 5, "both"), (16, 1, 64, "NHD")])
+    (2, 2, 16, "NHD"), (8, 2, 24, "HND"), (5, 5, 1, "NHD"), (7, 1, 5, "both"), (16, 1, 64, "NHD"),
+    (6, 3, 8, "both"), (4, 4, 32, "HND")])
 def test_decode(dtype, dim, heads, heads_kv, page, layout):
     run_decode(dtype, RAGGED, heads, heads_kv, dim, page, layout, seed=dim)
 

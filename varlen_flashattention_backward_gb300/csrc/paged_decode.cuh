@@ -188,15 +188,15 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// What a block in the ring is: x = mask of its keys | flags << 16, y = request,
-// z = segment inside the request.
+// What a block in the ring is: a mask of its keys, and these.
 enum : int {
   kPartBegins = 1 << 16,   // first block of a part
   kPartEnds = 1 << 17,
   kSegBegins = 1 << 18,    // first block of a segment
   kSegEnds = 1 << 19,
   kRangeEnds = 1 << 20,    // last block of the warp's range
-  kDone = 1 << 21          // no block: the range is done
+  kDone = 1 << 21,         // no block: the range is done
+  kRowsFetched = 1 << 22   // the part's query rows are in the place of its turn
 };
 
 // Shared memory of one kernel of NW warps: a ring of S stages (K and V block
@@ -216,7 +216,7 @@ struct Shape {
   // The kernels' static arrays, in the steps of the ring's alignment.
   static constexpr int static_bytes(int nw, int s) {
     const int nt = nw / TW;
-    return (nt * (R * 16 + 32) + nw * s * 16 + nt * s * 8 + 64 + 1023) / 1024 * 1024;
+    return (nt * (R * 16 + 32) + nt * s * 8 + 64 + 1023) / 1024 * 1024;
   }
   // Most stages, up to 8, that fit.
   static constexpr int fit(int nw, int qs) {
@@ -253,38 +253,33 @@ struct Tile {
 
 struct DecodeMaps {
   CUtensorMap k, v;
-  int axis[3];   // what the maps' axes 1 to 3 are: 0 head, 1 token, 2 page
+  int token_first;   // the maps' axes are dim, token, head, page, else dim, head, token, page
 };
 
-// One panel of KB tokens of one head.  The map's axes are the dims, then heads,
-// tokens and pages in the order of their strides.
-__device__ __forceinline__ void tma_load_panel(uint32_t dst, const CUtensorMap *map, uint32_t bar,
-                                               int x, int c1, int c2, int c3) {
+// One panel of KB tokens of one head, of K and of V.  All lanes execute it and one
+// issues.
+__device__ __forceinline__ void tma_load_panels_w(uint32_t dst_k, uint32_t dst_v,
+                                                  const DecodeMaps &maps, uint32_t bar, int x,
+                                                  int c1, int c2, int c3) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(c1), "r"(c2), "r"(c3)
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%2, {%5, %6, %7, %8}], [%4];\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%1], [%3, {%5, %6, %7, %8}], [%4];\n\t}" ::"r"(dst_k),
+      "r"(dst_v), "l"(reinterpret_cast<uint64_t>(&maps.k)),
+      "l"(reinterpret_cast<uint64_t>(&maps.v)), "r"(bar), "r"(x), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
 }
 constexpr long long kWaitNs = 2000000000LL;
 
 // The loading side of a team: walks its range and keeps the ring filled.
-// `look` finds the next block and starts the load of its page id (or ids);
-// `issue`, one block later, uses them to start the copies.  All warps of the team
-// walk alike.  With pages of whole blocks (kTma) one lane starts TMA copies of
-// whole panels; else the lanes copy 16 bytes at a time, each warp its share.
+// `look` finds the next block, `issue`, one block later, starts its copies.  All
+// warps of the team walk alike.  With pages of whole blocks (kTma) one lane starts
+// TMA copies of whole panels, and the lanes hold the page ids of 32 blocks; else
+// the lanes copy 16 bytes at a time, each warp its share, and hold the pages of
+// their rows.  This runs once per block in a warp that has but one other to hide
+// behind, so the usual step is kept short: some 40 instructions.
 template <typename T, int D, typename Sh, int RW, int TW, int KB, bool kTma>
 struct Loader {
   using Tl = Tile<D * int(sizeof(T)), KB>;
@@ -292,7 +287,7 @@ struct Loader {
   static constexpr int CPR = D / VEC;                   // 16-byte chunks per row
   static constexpr int kChunks = KB * CPR;              // ... and block
   static constexpr int kLoads = (kChunks + 32 * TW - 1) / (32 * TW);
-  static constexpr uint32_t kAll = (1u << KB) - 1;
+  static constexpr int kAll = (1 << KB) - 1;
   static_assert(KB <= 16, "decode block");
   const DecodeParams &p;
   const DecodeMaps &maps;
@@ -300,34 +295,37 @@ struct Loader {
   int left;                      // units left of the range
   int off, units, b, seg;        // units into the segment, and of it
   int blk, end;                  // next block of the part, and its end
-  bool begins;                   // blk begins its part
   Span span;
-  int4 desc;
-  int page, tok, head, err;
-  uint32_t rows_seen;            // mask of the looked-up block's rows that the query sees
-  int parts;                     // begun so far
-  int parts_free;                // ... and how many of them hold no query place any more
+  // The looked-up block: mask and flags, its request and segment, first row in the
+  // request and in its page.
+  int what, block_b, head, row, tok;
+  int id;                        // block_b * segs + segment
+  int page;                      // lane's page id ...
+  int page_lane;                 // ... and, kTma, whose is the block's
+  int err;
+  int parts, parts_free;         // begun so far, and how many hold no query place any more
+  int fifo_what, fifo_id;        // lane i: the block in stage i
 
   __device__ __forceinline__ Loader(const DecodeParams &p, const DecodeMaps &maps, int chunks)
       : p(p), maps(maps), chunks(chunks), segs(p.n_kv * chunks), lane(threadIdx.x & 31),
-        member((threadIdx.x >> 5) % TW), left(0), off(0), units(0), b(0), seg(0), blk(0), end(0),
-        begins(false), page(-1), tok(0), head(0), err(0), rows_seen(0), parts(0), parts_free(0) {
+        member((threadIdx.x >> 5) % TW), left(0), off(0), units(1), b(0), seg(0), blk(0), end(0),
+        what(0), block_b(0), head(0), row(0), tok(0), id(0), page(-1), page_lane(0), err(0),
+        parts(0), parts_free(0), fifo_what(kDone), fifo_id(0) {
     const int team = (threadIdx.x >> 5) / TW;
     if (p.direct) {
-      const int id = blockIdx.x / p.direct, teams = p.direct * Sh::NT;
-      b = id / segs;
-      seg = id - b * segs;
-      head = chunks == 1 ? seg : seg / chunks;
+      const int cta = blockIdx.x / p.direct, teams = p.direct * Sh::NT;
+      b = cta / segs;
+      seg = cta - b * segs;
       const int len = __ldg(p.lens + b);
       if ((len < 0 || len > p.max_pages * p.page_size) && p.error)
         atomicOr(p.error, FA_PAGED_BAD_LENGTH);
+      // Its share as a range whose units are blocks.
       span = span_of<KB>(p, len);
       const int per = (span.blocks + teams - 1) / teams;
-      blk = min((int(blockIdx.x) * Sh::NT + team - id * teams) * per, span.blocks);
-      end = min(blk + per, span.blocks);
-      begins = true;
-      desc.y = b;
-      desc.z = seg;
+      off = min((int(blockIdx.x) * Sh::NT + team - cta * teams) * per, span.blocks);
+      left = min(per, span.blocks - off);
+      off += kSwitchBlocks;
+      units = span.blocks + kSwitchBlocks;
       return;
     }
     const int range = blockIdx.x * Sh::NT + team;
@@ -348,100 +346,130 @@ struct Loader {
     units = units_of(p, span.blocks);
   }
 
-  __device__ __forceinline__ void look() {
-    while (blk >= end) {
-      if (left <= 0) {
-        desc.x = kDone;
-        return;
-      }
-      // The next part: the rest of the range inside the current segment.
-      const int upto = min(off + left, units);
-      blk = max((off << p.unit_shift) - kSwitchBlocks, 0);
-      end = min((upto << p.unit_shift) - kSwitchBlocks, span.blocks);
-      begins = true;
-      left -= upto - off;
-      off = upto;
-      if (blk >= end) continue;    // all of it is the segment's beginning
-      desc.y = b;
-      desc.z = seg;
-      head = chunks == 1 ? seg : seg / chunks;
-    }
-    const int j0 = (span.blk0 + blk) * KB;
-    const int n_lo = max(span.lo - j0, 0), n_hi = min(span.hi - j0, KB);
-    rows_seen = n_hi > n_lo ? (kAll >> (KB - n_hi)) & ~((1u << n_lo) - 1) : 0;
-    // With whole blocks every lane wants the page of the block's first row that
-    // counts, else lane r that of row r.
-    const int j = kTma ? j0 + n_lo : j0 + lane % KB;
-    if (kTma ? rows_seen != 0 : (rows_seen >> (lane % KB)) & 1) {
-      const int idx = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
-      tok = (kTma ? j0 : j) - idx * p.page_size;
-      page = p.table[desc.y * p.table_stride + idx];
-    }
-    desc.x = (begins ? kPartBegins : 0) | (blk == 0 ? kSegBegins : 0);
-    begins = false;
-    if (++blk >= end) {
-      desc.x |= kPartEnds | (end == span.blocks ? kSegEnds : 0) | (left == 0 ? kRangeEnds : 0);
-      if (off == units) {          // on to the next segment
+  __device__ __forceinline__ int page_index(int j) const {
+    return p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
+  }
+  // Lane i: the page of the block i behind the looked-up one.
+  __device__ __forceinline__ void load_pages() {
+    page_lane = 0;
+    const int j = row + lane * KB;
+    if (j < span.hi) page = __ldg(p.table + block_b * p.table_stride + page_index(j));
+  }
+
+  // The next part: the rest of the range inside the current segment.
+  __device__ __forceinline__ bool open_part() {
+    do {
+      if (left <= 0) return false;
+      if (off >= units) {          // on to the next segment
         off = 0;
         if (++seg == segs) {
           seg = 0;
-          if (++b >= p.batch) left = 0;
-          if (left > 0) enter();
+          if (++b >= p.batch) {
+            left = 0;
+            return false;
+          }
+          enter();
         }
+      }
+      const int upto = min(off + left, units);
+      blk = max((off << p.unit_shift) - kSwitchBlocks, 0);
+      end = min((upto << p.unit_shift) - kSwitchBlocks, span.blocks);
+      left -= upto - off;
+      off = upto;
+    } while (blk >= end);          // all of it is the segment's beginning
+    block_b = b;
+    head = chunks == 1 ? seg : seg / chunks;
+    id = b * segs + seg;
+    row = (span.blk0 + blk) * KB;
+    if constexpr (kTma) {
+      tok = row - page_index(row) * p.page_size;
+      load_pages();
+    }
+    return true;
+  }
+
+  __device__ __forceinline__ void look() {
+    what = 0;
+    if (blk >= end) {
+      if (!open_part()) {
+        what = kDone;
+        return;
+      }
+      what = kPartBegins | (blk == 0 ? kSegBegins : 0);
+    } else {
+      row += KB;
+      if constexpr (kTma) {
+        tok += KB;
+        if (tok >= p.page_size) tok = 0;
+        if (++page_lane == 32) load_pages();
+      }
+    }
+    if (row >= span.lo && row + KB <= span.hi) {
+      what |= kAll;
+    } else {
+      const int n_lo = max(span.lo - row, 0), n_hi = min(span.hi - row, KB);
+      if (n_hi > n_lo) what |= (kAll >> (KB - n_hi)) & ~((1 << n_lo) - 1);
+    }
+    if (++blk >= end)
+      what |= kPartEnds | (end == span.blocks ? kSegEnds : 0) | (left == 0 ? kRangeEnds : 0);
+    if constexpr (!kTma) {
+      if ((what >> (lane % KB)) & 1) {
+        const int j = row + lane % KB, idx = page_index(j);
+        tok = j - idx * p.page_size;
+        page = __ldg(p.table + block_b * p.table_stride + idx);
       }
     }
   }
 
-  // The part's query rows, if the warp has a free place: the copy's bytes.
-  __device__ __forceinline__ uint32_t query_rows(const T *&q, int q_bytes_max) const {
-    if (!(desc.x & kPartBegins) || !p.q_chunks || parts - parts_free >= Sh::QS) return 0;
-    const int h0 = (chunks == 1 ? 0 : desc.z % chunks * (RW * TW)) + member * RW;
-    q = static_cast<const T *>(p.q) + desc.y * p.q_stride + int64_t(head * p.group + h0) * D;
-    return uint32_t(min(max(p.group - h0, 0) * D * int(sizeof(T)), q_bytes_max));
-  }
-
-  // `dst`: the stage; `bar`: its barrier; `at`: where the warp keeps what the
-  // block is; `q_places`: the warp's places for query rows.
-  __device__ __forceinline__ void issue(uint32_t dst, uint32_t bar, int4 *at,
+  // `dst`: the stage, number `stage`; `bar`: its barrier; `q_places`: the warp's
+  // places for query rows.
+  __device__ __forceinline__ void issue(int stage, uint32_t dst, uint32_t bar,
                                         uint32_t q_places) {
-    if (desc.x & kDone) {
-      if (lane == 0) *at = make_int4(kDone, 0, 0, 0);
+    if (what & kDone) {
+      if (lane == stage) fifo_what = kDone;
     } else {
+      // The part's query rows, if the warp has a free place.
       const T *q = nullptr;
-      const uint32_t q_bytes = query_rows(q, Sh::kQ);
-      const uint32_t q_to = q_places + (parts % (Sh::QS > 0 ? Sh::QS : 1)) * Sh::kQ;
-      if (desc.x & kPartBegins) ++parts;
-      const bool fine = page >= 0 && page < p.num_pages;
-      if constexpr (kTma) {
-        const uint32_t mask = fine ? rows_seen : 0;
-        if (rows_seen != mask) err = FA_PAGED_BAD_PAGE;
-        if (lane == 0) {
-          *at = make_int4(desc.x | int(mask), desc.y, desc.z, q_bytes != 0);
-          const bool copies = mask != 0 && member == 0;
-          mbar_arrive_expect_tx(bar, (copies ? Sh::kStage : 0) + q_bytes);
-          if (copies) {
-            const auto at = [&](int axis) { return axis == 0 ? head : axis == 1 ? tok : page; };
-            const int c1 = at(maps.axis[0]), c2 = at(maps.axis[1]), c3 = at(maps.axis[2]);
-#pragma unroll
-            for (int i = 0; i < CPR / Tl::CPP; ++i) {
-              const int x = i * Tl::CPP * VEC;
-              const uint32_t to = dst + i * KB * Tl::PB;
-              tma_load_panel(to, &maps.k, bar, x, c1, c2, c3);
-              tma_load_panel(to + Sh::kBlock, &maps.v, bar, x, c1, c2, c3);
-            }
-          }
-          if (q_bytes) bulk_load(q_to, q, q_bytes, bar);
+      uint32_t q_bytes = 0, q_to = 0;
+      if (what & kPartBegins) {
+        if (p.q_chunks && parts - parts_free < Sh::QS) {
+          const int h0 = (chunks == 1 ? 0 : (id - block_b * segs) % chunks * (RW * TW)) +
+                         member * RW;
+          q = static_cast<const T *>(p.q) + block_b * p.q_stride +
+              int64_t(head * p.group + h0) * D;
+          q_bytes = uint32_t(min(max(p.group - h0, 0), RW) * D * int(sizeof(T)));
+          q_to = q_places + (parts % (Sh::QS > 0 ? Sh::QS : 1)) * Sh::kQ;
+          if (q_bytes) what |= kRowsFetched;
         }
+        ++parts;
+      }
+      if constexpr (kTma) {
+        const int my_page = __shfl_sync(kFull, page, page_lane);
+        if (uint32_t(my_page) >= uint32_t(p.num_pages)) {
+          if (what & kAll) err = FA_PAGED_BAD_PAGE;
+          what &= ~kAll;
+        }
+        const bool copies = (TW == 1 || member == 0) && (what & kAll);
+        sm103::mbar_arrive_expect_tx_w(bar, (copies ? Sh::kStage : 0) + q_bytes);
+        if (copies) {
+          const int c1 = maps.token_first ? tok : head, c2 = maps.token_first ? head : tok;
+#pragma unroll
+          for (int i = 0; i < CPR / Tl::CPP; ++i)
+            tma_load_panels_w(dst + i * KB * Tl::PB, dst + Sh::kBlock + i * KB * Tl::PB, maps, bar,
+                              i * Tl::CPP * VEC, c1, c2, my_page);
+        }
+        if (q_bytes) sm103::bulk_load_w(q_to, q, q_bytes, bar);
       } else {
-        const uint32_t mask = rows_seen & __ballot_sync(kFull, fine);
-        if (rows_seen != mask) err = FA_PAGED_BAD_PAGE;
-        if (lane == 0) *at = make_int4(desc.x | int(mask), desc.y, desc.z, q_bytes != 0);
-        const int64_t row =
+        const bool fine = uint32_t(page) < uint32_t(p.num_pages);
+        const int mask = what & kAll & __ballot_sync(kFull, fine);
+        if (mask != (what & kAll)) err = FA_PAGED_BAD_PAGE;
+        what = (what & ~kAll) | mask;
+        const int64_t at =
             fine ? page * p.page_stride + tok * p.token_stride + head * p.head_stride : 0;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
           const int c = (i * TW + member) * 32 + lane, r = c / CPR, ch = c % CPR;
-          const int64_t o = __shfl_sync(kFull, row, r % KB);
+          const int64_t o = __shfl_sync(kFull, at, r % KB);
           const bool take = (mask >> (r % KB)) & 1;
           if (kChunks % (32 * TW) == 0 || c < kChunks) {
             const int64_t from = (take ? o : 0) + ch * VEC;
@@ -451,6 +479,10 @@ struct Loader {
         }
         for (int i = lane; i < int(q_bytes) / 16; i += 32)
           cp_async16(q_to + i * 16, q + i * VEC, true);
+      }
+      if (lane == stage) {
+        fifo_what = what;
+        fifo_id = id;
       }
     }
     if constexpr (!kTma) cp_async_commit();
@@ -693,21 +725,26 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
+// c += a b, or c = a b.
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
+                                         uint32_t b1, bool first = false) {
+  const float z0 = first ? 0.f : c[0], z1 = first ? 0.f : c[1], z2 = first ? 0.f : c[2],
+              z3 = first ? 0.f : c[3];
   if constexpr (std::is_same<T, __nv_bfloat16>::value)
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(z0), "f"(z1), "f"(z2),
+          "f"(z3));
   else
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(z0), "f"(z1), "f"(z2),
+          "f"(z3));
 }
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -748,7 +785,6 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   constexpr int NR = RW / 8;        // rows of a lane
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Partials<NT, R> s_part;
-  __shared__ int4 s_desc[NW][S];
   __shared__ uint64_t s_full[NT][S];
   __shared__ int s_abort;
   asm volatile("griddepcontrol.launch_dependents;");
@@ -780,15 +816,18 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   load.look();
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) {
-    load.issue(ring + i * Sh::kStage, full + i * 8, &s_desc[warp][i], q_places);
+    load.issue(i, ring + i * Sh::kStage, full + i * 8, q_places);
     load.look();
   }
 
   const int row = lane >> 2, col = (lane & 3) * 2;
-  // ldmatrix addresses inside a block: K (n = key, k = dim) and V (transposed).
-  const int k_row = (lane & 7) + ((lane >> 4) << 3), k_ch = (lane >> 3) & 1;
-  const int v_row = (lane & 7) + (((lane >> 3) & 1) << 3), v_ch = lane >> 4;
-  int stage = 0, fill = S - 1, heads = 0, n0 = 0;
+  // ldmatrix addresses inside a block, K (n = key, k = dim) and V (transposed), of
+  // chunk pairs: pair c of a panel is at the first one's address ^ 32 c, since
+  // panels' rows begin at multiples of their length.
+  constexpr int kPairs = Tl::CPP / 2;              // per panel
+  const int k_at = Tl::at((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+  const int v_at = Tl::at((lane & 7) + (((lane >> 3) & 1) << 3), lane >> 4);
+  int stage = 0, fill = S - 1, heads = 0, n0 = 0, id = 0, b = 0;
   uint32_t parity = 0;
   uint32_t qa[D / 16][2 * NR];
   float o[D / 8][4];
@@ -799,18 +838,20 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   while (true) {
     if constexpr (!kTma) cp_async_wait<S - 2>();
     team_sync<TW>();                // the stage to fill has been read
-    const int4 desc = s_desc[warp][stage];
-    if (desc.x & kDone) break;
+    const int what = __shfl_sync(kFull, load.fifo_what, stage);
+    if (what & kDone) break;
     if constexpr (kTma) wait_stage(full + stage * 8, parity, &s_abort);
     const uint32_t kb = ring + stage * Sh::kStage, vb = kb + Sh::kBlock;
 
-    if (desc.x & kPartBegins) {
-      opens = desc.x & kSegBegins;
-      const int hk = chunks == 1 ? desc.z : desc.z / chunks;
-      const int h0 = (chunks == 1 ? 0 : (desc.z - hk * chunks) * R) + row0;
+    if (what & kPartBegins) {
+      opens = what & kSegBegins;
+      id = __shfl_sync(kFull, load.fifo_id, stage);
+      b = id / segs;
+      const int seg = id - b * segs, hk = chunks == 1 ? seg : seg / chunks;
+      const int h0 = (chunks == 1 ? 0 : (seg - hk * chunks) * R) + row0;
       heads = min(RW, p.group - h0);           // may be negative
       n0 = hk * p.group + h0;
-      if (desc.w) {
+      if (what & kRowsFetched) {
         // Fragments by ldmatrix: rows behind the last head hold anything, and
         // nothing reads their results.
         const uint32_t qs = q_places + load.parts_free % (Sh::QS > 0 ? Sh::QS : 1) * Sh::kQ;
@@ -833,7 +874,7 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
         __syncwarp();               // the place is free
       } else {
         // Rows behind the last head repeat it.
-        const T *qr = q + desc.y * p.q_stride + int64_t(n0 - row0) * D;
+        const T *qr = q + b * p.q_stride + int64_t(n0 - row0) * D;
 #pragma unroll
         for (int i = 0; i < 2 * NR; ++i) {
           // Fragment i of a step: rows row (and row + 8 for odd i with 16).
@@ -857,14 +898,14 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
         l[i] = 0.f;
       }
     }
-    load.issue(ring + fill * Sh::kStage, full + fill * 8, &s_desc[warp][fill], q_places);
+    load.issue(fill, ring + fill * Sh::kStage, full + fill * 8, q_places);
     load.look();
     fill = fill + 1 == S ? 0 : fill + 1;
     if (++stage == S) {
       stage = 0;
       parity ^= 1;
     }
-    const uint32_t mask = desc.x & 0xffff;
+    const int mask = what & 0xffff;
     if (kTma && mask != 0xffff) {
       clear_rows<D * 2, KB>(my + (vb - ring), mask);
       team_sync<TW>();
@@ -872,11 +913,9 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
 
     float sa[2][2][4];              // [chain][key half][fragment]
 #pragma unroll
-    for (int i = 0; i < 16; ++i) (&sa[0][0][0])[i] = 0.f;
-#pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       uint32_t kf[4];
-      ldsm4(kf, kb + Tl::at(k_row, ks * 2 + k_ch));
+      ldsm4(kf, (kb + ks / kPairs * (KB * Tl::PB) + k_at) ^ (ks % kPairs * 32));
       uint32_t a[4];
       if constexpr (NR == 1) {
         a[0] = qa[ks][0];
@@ -887,23 +926,28 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] = qa[ks][i];
       }
-      mma16816<T>(sa[ks & 1][0], a, kf[0], kf[1]);
-      mma16816<T>(sa[ks & 1][1], a, kf[2], kf[3]);
+      mma16816<T>(sa[ks & 1][0], a, kf[0], kf[1], ks < 2);
+      mma16816<T>(sa[ks & 1][1], a, kf[2], kf[3], ks < 2);
     }
     float s[NR][4];                 // keys col, col + 1, col + 8, col + 9
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        s[i][e] = (sa[0][e >> 1][i * 2 + (e & 1)] + sa[1][e >> 1][i * 2 + (e & 1)]) * p.scale_log2;
+    if (mask != 0xffff) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (!((mask >> (col + (e & 1) + (e >> 1) * 8)) & 1)) {
+#pragma unroll
+          for (int i = 0; i < NR; ++i) s[i][e] = -CUDART_INF_F;
+        }
+    }
     float mn[NR];
     bool grows = false;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      float t = -CUDART_INF_F;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int key = col + (e & 1) + (e >> 1) * 8;
-        const float x = (sa[0][e >> 1][i * 2 + (e & 1)] + sa[1][e >> 1][i * 2 + (e & 1)]) *
-                        p.scale_log2;
-        s[i][e] = (desc.x >> key) & 1 ? x : -CUDART_INF_F;
-        t = fmaxf(t, s[i][e]);
-      }
+      float t = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
       t = fmaxf(t, __shfl_xor_sync(kFull, t, 1));
       t = fmaxf(t, __shfl_xor_sync(kFull, t, 2));
       mn[i] = fmaxf(m[i], t);
@@ -944,7 +988,7 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
 #pragma unroll
     for (int dt = 0; dt < D / 16; ++dt) {
       uint32_t vf[4];
-      ldsm4_t(vf, vb + Tl::at(v_row, dt * 2 + v_ch));
+      ldsm4_t(vf, (vb + dt / kPairs * (KB * Tl::PB) + v_at) ^ (dt % kPairs * 32));
       if constexpr (NR == 1) {
         const uint32_t a[4] = {hi[0][0], lo[0][0], hi[0][1], lo[0][1]};
         mma16816<T>(o[2 * dt], a, vf[0], vf[1]);
@@ -961,21 +1005,20 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
 
     if (kTma && mask != 0xffff) sm103::fence_proxy_async_smem();   // before the next copy there
 
-    if (desc.x & kPartEnds) {
-      const bool ends = desc.x & kSegEnds;
+    if (what & kPartEnds) {
+      const bool ends = what & kSegEnds;
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
         l[i] += __shfl_xor_sync(kFull, l[i], 1);
         l[i] += __shfl_xor_sync(kFull, l[i], 2);
       }
-      const int id = desc.y * segs + desc.z;
       if (opens && ends) {
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
           const int r = row + i * 8;
           if (r >= heads) continue;
           const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
-          T *y = static_cast<T *>(p.y) + desc.y * p.y_stride + int64_t(n0 + r) * D + col;
+          T *y = static_cast<T *>(p.y) + b * p.y_stride + int64_t(n0 + r) * D + col;
 #pragma unroll
           for (int k = 0; k < D / 8; ++k) {
             const float x0 = (NR == 1 ? o[k][0] + o[k][2] : o[k][i * 2]) * inv;
@@ -987,12 +1030,12 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
               y[k * 8 + 1] = from_f<T>(x1);
             }
           }
-          if ((lane & 3) == 0) write_stats(p, desc.y, n0 + r, m[i] * kLn2, l[i]);
+          if ((lane & 3) == 0) write_stats(p, b, n0 + r, m[i] * kLn2, l[i]);
         }
       } else {
         team_sync<TW>();            // the ring has been read
         const int slot = opens ? 1 : 0;
-        float *dst = partial_at<NT, TW>(p, R, desc.x & kRangeEnds, my);
+        float *dst = partial_at<NT, TW>(p, R, what & kRangeEnds, my);
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
           const int r = row0 + row + i * 8;
@@ -1047,7 +1090,6 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
   constexpr int NV = D / (32 * VW);                             // accesses per row
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Partials<NW, R> s_part;
-  __shared__ int4 s_desc[NW][S];
   __shared__ uint64_t s_full[NW][S];
   __shared__ int s_abort;
   asm volatile("griddepcontrol.launch_dependents;");
@@ -1080,12 +1122,12 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
   load.look();
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) {
-    load.issue(ring + i * Sh::kStage, full + i * 8, &s_desc[warp][i], q_places);
+    load.issue(i, ring + i * Sh::kStage, full + i * 8, q_places);
     load.look();
   }
 
   const int key = lane >> 2, quarter = lane & 3;
-  int stage = 0, fill = S - 1, heads = 0, n0 = 0;
+  int stage = 0, fill = S - 1, heads = 0, n0 = 0, id = 0, b = 0;
   uint32_t parity = 0;
   float o[R][NV * VW], m[R], l[R];
   bool opens = false;
@@ -1094,30 +1136,32 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
   while (true) {
     if constexpr (!kTma) cp_async_wait<S - 2>();
     __syncwarp();                    // the stage to fill has been read
-    const int4 desc = s_desc[warp][stage];
-    if (desc.x & kDone) break;
+    const int what = __shfl_sync(kFull, load.fifo_what, stage);
+    if (what & kDone) break;
+    if (what & kPartBegins) id = __shfl_sync(kFull, load.fifo_id, stage);
     if constexpr (kTma) wait_stage(full + stage * 8, parity, &s_abort);
     uint8_t *kb = my + stage * Sh::kStage, *vb = kb + Sh::kBlock;
-    load.issue(ring + fill * Sh::kStage, full + fill * 8, &s_desc[warp][fill], q_places);
+    load.issue(fill, ring + fill * Sh::kStage, full + fill * 8, q_places);
     load.look();
     fill = fill + 1 == S ? 0 : fill + 1;
     if (++stage == S) {
       stage = 0;
       parity ^= 1;
     }
-    const uint32_t mask = desc.x & 0xff;
+    const int mask = what & 0xff;
     if (kTma && mask != 0xff) clear_rows<D * 4, KB>(vb, mask);
 
-    if (desc.x & kPartBegins) {
-      opens = desc.x & kSegBegins;
-      const int hk = chunks == 1 ? desc.z : desc.z / chunks;
-      const int h0 = chunks == 1 ? 0 : (desc.z - hk * chunks) * R;
+    if (what & kPartBegins) {
+      opens = what & kSegBegins;
+      b = id / segs;
+      const int seg = id - b * segs, hk = chunks == 1 ? seg : seg / chunks;
+      const int h0 = chunks == 1 ? 0 : (seg - hk * chunks) * R;
       heads = min(R, p.group - h0);
       n0 = hk * p.group + h0;
       // A part keeps its place until it ends.
       s_q = reinterpret_cast<float *>(extra + load.parts_free % Sh::QS * Sh::kQ);
-      if (!desc.w) {
-        const float *qr = static_cast<const float *>(p.q) + desc.y * p.q_stride + int64_t(n0) * D;
+      if (!(what & kRowsFetched)) {
+        const float *qr = static_cast<const float *>(p.q) + b * p.q_stride + int64_t(n0) * D;
         for (int i = lane; i < heads * D; i += 32) s_q[i] = __ldg(qr + i);
         if (kTma) sm103::fence_proxy_async_smem();   // before a later copy to this place
         __syncwarp();
@@ -1148,7 +1192,7 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
         s[r] = fmaf(kv.w, qv.w, s[r]);
       }
     }
-    const bool ok = (desc.x >> key) & 1;
+    const bool ok = (what >> key) & 1;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       s[r] += __shfl_xor_sync(kFull, s[r], 1);
@@ -1201,10 +1245,9 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
 
     if (kTma && mask != 0xff) sm103::fence_proxy_async_smem();   // before the next copy there
 
-    if (desc.x & kPartEnds) {
+    if (what & kPartEnds) {
       ++load.parts_free;
-      const bool ends = desc.x & kSegEnds;
-      const int id = desc.y * segs + desc.z;
+      const bool ends = what & kSegEnds;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
 #pragma unroll
@@ -1213,12 +1256,12 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
       const bool whole = opens && ends;
       const int slot = opens ? 1 : 0;
       __syncwarp();                  // the ring has been read
-      float *dst = partial_at<NW, 1>(p, R, desc.x & kRangeEnds, my);
+      float *dst = partial_at<NW, 1>(p, R, what & kRangeEnds, my);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (r >= heads) continue;
         const float inv = whole ? (l[r] == 0.f ? 0.f : 1.f / l[r]) : 1.f;
-        float *to = whole ? static_cast<float *>(p.y) + desc.y * p.y_stride + int64_t(n0 + r) * D
+        float *to = whole ? static_cast<float *>(p.y) + b * p.y_stride + int64_t(n0 + r) * D
                           : dst + r * (D + Sh::PAD);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -1226,7 +1269,7 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
           for (int e = 0; e < VW; ++e) to[(i * 32 + lane) * VW + e] = o[r][i * VW + e] * inv;
         if (lane == 0) {
           if (whole) {
-            write_stats(p, desc.y, n0 + r, m[r] * kLn2, l[r]);
+            write_stats(p, b, n0 + r, m[r] * kLn2, l[r]);
           } else {
             s_part.m[slot][warp][r] = m[r];
             s_part.l[slot][warp][r] = l[r];
@@ -1374,36 +1417,27 @@ bool make_page_maps(DecodeMaps &maps, const DecodeParams &p) {
   if (enc == nullptr || p.page_size % KB != 0) return false;
   const int64_t count[3] = {p.n_kv, p.page_size, p.num_pages};
   const int64_t stride[3] = {p.head_stride, p.token_stride, p.page_stride};
-  // By stride, axes of one entry (whose stride is 0 here) last.
-  int order[3] = {0, 1, 2};
-  const auto later = [&](int a, int b) {
-    if ((count[a] == 1) != (count[b] == 1)) return count[a] == 1;
-    return stride[a] > stride[b];
-  };
-  for (int i = 0; i < 2; ++i)
-    for (int k = 0; k < 2 - i; ++k)
-      if (later(order[k], order[k + 1])) {
-        const int t = order[k];
-        order[k] = order[k + 1];
-        order[k + 1] = t;
-      }
   cuuint64_t dims[4] = {D}, strides[3];
   cuuint32_t box[4] = {Tl::PB / sizeof(T), 1, 1, 1};
-  int64_t inner = 1, extent = D;   // stride and extent of the axis before, in elements
-  for (int i = 0; i < 3; ++i) {
-    const int a = order[i];
-    const int64_t own = count[a] == 1 ? extent : stride[a];
-    if (own < extent || (i > 0 && own % inner != 0) ||
-        own * int64_t(sizeof(T)) >= (int64_t(1) << 40) || count[a] > (int64_t(1) << 31))
-      return false;
-    inner = own;
-    extent = own * count[a];
-    dims[i + 1] = cuuint64_t(count[a]);
-    strides[i] = cuuint64_t(own) * sizeof(T);
-    if (strides[i] % 16 != 0) return false;
-    if (a == 1) box[i + 1] = KB;
-    maps.axis[i] = a;
-  }
+  const auto nested = [&](bool token_first) {
+    const int order[3] = {token_first ? 1 : 0, token_first ? 0 : 1, 2};
+    int64_t inner = 1, extent = D;   // stride and extent of the axis before, in elements
+    for (int i = 0; i < 3; ++i) {
+      const int a = order[i];
+      const int64_t own = count[a] == 1 ? extent : stride[a];   // (an axis of one: any will do)
+      if (own < extent || own % inner != 0 || own * int64_t(sizeof(T)) % 16 != 0 ||
+          own * int64_t(sizeof(T)) >= (int64_t(1) << 40))
+        return false;
+      inner = own;
+      extent = own * count[a];
+      dims[i + 1] = cuuint64_t(count[a]);
+      strides[i] = cuuint64_t(own) * sizeof(T);
+      box[i + 1] = a == 1 ? KB : 1;
+    }
+    maps.token_first = token_first;
+    return true;
+  };
+  if (!nested(false) && !nested(true)) return false;
   const cuuint32_t ones[4] = {1, 1, 1, 1};
   const CUtensorMapDataType type = std::is_same<T, float>::value    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
