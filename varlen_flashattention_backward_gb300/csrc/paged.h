@@ -47,8 +47,8 @@ struct DecodeParams {
   int64_t y_stride;
   float *smax, *ssum;
   int32_t *error;
-  float *part;        // partial results: two slots per CTA (see paged_decode.cuh)
-  float *team_part;   // ... and one per team
+  float *part;        // partial results: two slots per range (see paged_decode.cuh)
+  int slot_rows;      // query heads in a slot
   int num_pages, page_size, page_shift;   // page_shift: log2(page_size), or -1
   int max_pages, batch, n, n_kv, d, group;
   int y_pairs;            // rows of y start on 4-byte boundaries

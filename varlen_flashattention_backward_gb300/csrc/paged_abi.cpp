@@ -98,18 +98,13 @@ int log2_or_none(int64_t x) {
   return n;
 }
 
-struct DecodeLayout {
-  size_t part, team_part, total;
-};
-
-// Two partial results per CTA and one per team; none for a direct call.
-DecodeLayout decode_layout(const DecodePlan &plan, int ctas, int64_t head_dim) {
-  const size_t slot = decode_part_floats(plan.rows, int(head_dim)) * sizeof(float);
-  DecodeLayout L;
-  L.part = 0;
-  L.team_part = align_up(size_t(ctas) * 2 * slot);
-  L.total = plan.direct ? 0 : L.team_part + align_up(size_t(ctas) * plan.teams * slot);
-  return L;
+// Bytes of a decode call's workspace: two partial results per range, none for a
+// direct call.
+size_t decode_bytes(const DecodePlan &plan, int sms, int group, int64_t head_dim) {
+  if (plan.direct) return 0;
+  const int rows = group < plan.rows ? group : plan.rows;
+  return align_up(size_t(sms) * plan.teams * 2 * decode_part_floats(rows, int(head_dim)) *
+                  sizeof(float));
 }
 
 // Keys that a query can see at most.
@@ -214,7 +209,7 @@ fa_status fa_paged_decode_workspace_size(int64_t batch, int64_t head_num, int64_
   const DecodePlan plan = decode_plan(dtype, int(batch), int(head_num_kv),
                                       int(head_num / head_num_kv), int(head_dim),
                                       most_keys(max_pages, page_size, pre_tokens), sms);
-  *workspace_bytes = decode_layout(plan, sms, head_dim).total;
+  *workspace_bytes = decode_bytes(plan, sms, int(head_num / head_num_kv), head_dim);
   return FA_OK;
 }
 
@@ -246,10 +241,10 @@ fa_status fa_paged_decode(const void *q, int64_t q_stride, const void *k_pages,
   const DecodePlan plan =
       decode_plan(dtype, int(batch), int(head_num_kv), group, int(head_dim),
                   most_keys(max_pages, page_size, pre_tokens), sms);
-  const DecodeLayout L = decode_layout(plan, sms, head_dim);
-  if (L.total > 0 && !workspace) return FA_ERR_NULLPTR;
+  const size_t bytes = decode_bytes(plan, sms, group, head_dim);
+  if (bytes > 0 && !workspace) return FA_ERR_NULLPTR;
   if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return FA_ERR_INVALID;
-  if (workspace_bytes < L.total) return FA_ERR_WORKSPACE;
+  if (workspace_bytes < bytes) return FA_ERR_WORKSPACE;
 
   DecodeParams p{};
   p.q = q;
@@ -267,8 +262,8 @@ fa_status fa_paged_decode(const void *q, int64_t q_stride, const void *k_pages,
   p.smax = softmax_max;
   p.ssum = softmax_sum;
   p.error = error;
-  p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.part);
-  p.team_part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.team_part);
+  p.part = static_cast<float *>(workspace);
+  p.slot_rows = group < plan.rows ? group : plan.rows;
   p.num_pages = int(num_pages);
   p.page_size = int(page_size);
   p.page_shift = log2_or_none(page_size);

@@ -36,16 +36,14 @@ constexpr int kDirectBlocks = 4;
 //
 // A team's share of a segment is a part.  A part that is a whole segment
 // writes y from the warps' registers.  Of the others a team has at most two,
-// its first (slot A, where it does not begin its segment) and its last (slot B,
-// where it does); they wait until the CTA's teams are done, when neighbouring
-// parts of one segment are added.  What then still misses a neighbour, at most
-// two sums per CTA, goes to the workspace: slot 0 where it does not begin its
-// segment, slot 1 where it does.  join_kernel adds those, in order.
+// its first (slot 0, where it does not begin its segment) and its last (slot 1,
+// where it does), which go to the range's slots in the workspace.  join_kernel
+// adds the parts of a segment, in order.
 //
-// Where there are few segments and none can be long (direct_ctas), a segment
-// gets a cluster of CTAs instead: its blocks are dealt to their teams, and the
-// CTAs' sums are added through distributed shared memory.  That saves finding
-// the ranges, the workspace and the second kernel.
+// Where there are few segments and none can be long (decode_plan), a segment gets
+// a cluster of CTAs instead: its blocks are dealt to their teams, whose parts are
+// added in shared memory, and the CTAs' sums through distributed shared memory.
+// That saves finding the ranges, the workspace and the second kernel.
 // ---------------------------------------------------------------------------
 struct Span {
   int lo, hi;        // keys [lo, hi) that the query sees
@@ -216,7 +214,7 @@ struct Shape {
   // The kernels' static arrays, in the steps of the ring's alignment.
   static constexpr int static_bytes(int nw, int s) {
     const int nt = nw / TW;
-    return (nt * (R * 16 + 32) + nt * s * 8 + 64 + 1023) / 1024 * 1024;
+    return (nt * (R * 8 + 4) + nt * s * 8 + 64 + 1023) / 1024 * 1024;
   }
   // Most stages, up to 8, that fit.
   static constexpr int fit(int nw, int qs) {
@@ -529,8 +527,8 @@ __device__ __forceinline__ void team_sync() {
 // Floats of one workspace slot: o [rows][d], then the rows' maxima and sums.
 __host__ __device__ constexpr int slot_floats(int rows, int d) { return rows * (d + 4); }
 
-__device__ __forceinline__ float *slot_of(const DecodeParams &p, int cta, int slot, int rows) {
-  return p.part + (int64_t(cta) * 2 + slot) * slot_floats(rows, p.d);
+__device__ __forceinline__ float *slot_of(const DecodeParams &p, int range, int slot) {
+  return p.part + (int64_t(range) * 2 + slot) * slot_floats(p.slot_rows, p.d);
 }
 
 __device__ __forceinline__ void write_stats(const DecodeParams &p, int b, int n, float mx,
@@ -544,107 +542,62 @@ __device__ __forceinline__ void write_stats(const DecodeParams &p, int b, int n,
   }
 }
 
-// The partial results of a CTA's teams: slot A of the part that does not begin
-// its segment, slot B of the part that does and does not end it.
+// The parts of a direct call's CTA, one per team: o in the team's ring, which is
+// free by then.
 template <int NT, int R>
 struct Partials {
-  float m[2][NT][R], l[2][NT][R];
-  const float *o[2][NT];            // [R][D + PAD]
-  int id[2][NT];                    // segment (b * segs + seg), or -1
-  int ends[2][NT];                  // whether the part ends it
+  float m[NT][R], l[NT][R];
+  int state[NT];                    // kHas | kSegBegins | kSegEnds of the part
 };
+constexpr int kHas = 1;
 
-// Where a team puts the partial result of a part: its ring when the part is
-// the last of its range (nothing is on the way behind it), else, so for a slot A
-// that more parts follow, its place in the workspace.
-template <int NT, int TW>
-__device__ __forceinline__ float *partial_at(const DecodeParams &p, int rows, bool last,
-                                             uint8_t *ring) {
-  if (last) return reinterpret_cast<float *>(ring);
-  return p.team_part +
-         (int64_t(blockIdx.x) * NT + (threadIdx.x >> 5) / TW) * slot_floats(rows, p.d);
-}
-
-// Adds neighbouring partial results (see the top) once every team is done.  A
-// run begins with team 0's slot A or any team's slot B and goes on with the
-// slots A of the teams behind it.  A warp takes one row of one run at a time.
-template <typename T, int D, int R, int NW, int NT, int PAD>
-__device__ __forceinline__ void merge_partials(const DecodeParams &p, int chunks,
-                                               const Partials<NT, R> &s, float *cta_part) {
+// Adds the parts of a direct call's CTA, which are those of its first teams.  A
+// warp takes one row at a time.  The sum goes to y if it is the whole segment, else
+// to `cta_part`.
+template <typename T, int D, int R, typename Sh>
+__device__ __forceinline__ void merge_cta(const DecodeParams &p, int chunks,
+                                          const Partials<Sh::NT, R> &s, const uint8_t *rings,
+                                          float *cta_part) {
+  constexpr int NT = Sh::NT, PITCH = D + Sh::PAD;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = min(R, p.group);
-  // Lane k < NT: the id in team k's slot A, lane 16 + k: in its slot B.
-  const int id_of = (lane & 15) < NT ? s.id[lane >> 4][lane & 15] : -1;
-  const uint32_t held = __ballot_sync(kFull, id_of >= 0);
-  uint32_t runs = held & 0xffff0001u;
-  const int tasks = __popc(runs) * rows;
+  const int state = lane < NT ? s.state[lane] : 0;
+  const int count = __popc(__ballot_sync(kFull, state & kHas));
+  if (count == 0) return;
+  const bool whole = __any_sync(kFull, state & kSegBegins) && __any_sync(kFull, state & kSegEnds);
+  const int segs = p.n_kv * chunks, id = blockIdx.x / p.direct, b = id / segs, seg = id - b * segs;
+  const int hk = chunks == 1 ? seg : seg / chunks, h0 = (seg - hk * chunks) * R;
+  const int n0 = hk * p.group + h0, rows = min(R, p.group - h0);
 #pragma unroll 1
-  for (int task = warp; task < tasks; task += NW) {
-    const int run = task / rows, r = task - run * rows;
-    uint32_t rest = runs;
-    for (int i = 0; i < run; ++i) rest &= rest - 1;
-    const int at = __ffs(rest) - 1, slot = at >> 4, w0 = at & 15;
-    // Its members: w0, then the slots A behind it up to the first gap or the
-    // first that ends the segment.
-    int count = 1;
-    bool ends = s.ends[slot][w0];
-    while (!ends && w0 + count < NT) {
-      ends = s.ends[0][w0 + count];
-      ++count;
-    }
-    const int id = __shfl_sync(kFull, id_of, at);
-    const int segs = p.n_kv * chunks;
-    const int b = id / segs, seg = id - b * segs;
-    const int h = (chunks == 1 ? 0 : seg % chunks * R) + r;
-    if (h >= p.group) continue;
-    const int n = (chunks == 1 ? seg : seg / chunks) * p.group + h;
+  for (int r = warp; r < rows; r += Sh::NW) {
     const int mine = lane < count ? lane : 0;
-    const int my_slot = mine == 0 ? slot : 0;
-    const float m = s.m[my_slot][w0 + mine][r], l = s.l[my_slot][w0 + mine][r];
+    const float m = s.m[mine][r], l = s.l[mine][r];
     float mx = m;
 #pragma unroll
-    for (int o = 1; o < NT; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
     const float f = sm103::ex2(m - (mx == -CUDART_INF_F ? 0.f : mx));
-    float sum = 0.f;
-    const bool whole = slot == 1 && ends;
-    float *dst = p.direct ? cta_part : slot_of(p, blockIdx.x, slot, R);
+    float sum = 0.f, acc[D / 32];
 #pragma unroll
-    for (int d0 = 0; d0 < D; d0 += 128) {
-      const int d = d0 + lane * 4;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      sum = 0.f;
+    for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
 #pragma unroll 2
-      for (int k = 0; k < count; ++k) {
-        const float fk = __shfl_sync(kFull, f, k);
-        sum += fk * __shfl_sync(kFull, l, k);
-        if (d < D) {
-          const float4 o = *reinterpret_cast<const float4 *>(
-              s.o[k == 0 ? slot : 0][w0 + k] + r * (D + PAD) + d);
-          acc.x += fk * o.x;
-          acc.y += fk * o.y;
-          acc.z += fk * o.z;
-          acc.w += fk * o.w;
-        }
-      }
-      if (d < D) {
-        if (whole) {
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          T *y = static_cast<T *>(p.y) + b * p.y_stride + int64_t(n) * D + d;
-          y[0] = from_f<T>(acc.x * inv);
-          y[1] = from_f<T>(acc.y * inv);
-          y[2] = from_f<T>(acc.z * inv);
-          y[3] = from_f<T>(acc.w * inv);
-        } else {
-          *reinterpret_cast<float4 *>(dst + r * D + d) = acc;
-        }
-      }
+    for (int k = 0; k < count; ++k) {
+      const float fk = __shfl_sync(kFull, f, k);
+      sum += fk * __shfl_sync(kFull, l, k);
+      const float *o = reinterpret_cast<const float *>(rings + k * Sh::kRing) + r * PITCH + lane;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) acc[i] += fk * o[32 * i];
     }
-    if (lane == 0) {
-      if (whole) {
-        write_stats(p, b, n, mx * kLn2, sum);
-      } else {
-        dst[R * D + r] = mx;
-        dst[R * D + R + r] = sum;
+    if (whole) {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      T *y = static_cast<T *>(p.y) + b * p.y_stride + int64_t(n0 + r) * D + lane;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) y[32 * i] = from_f<T>(acc[i] * inv);
+      if (lane == 0) write_stats(p, b, n0 + r, mx * kLn2, sum);
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) cta_part[r * D + lane + 32 * i] = acc[i];
+      if (lane == 0) {
+        cta_part[R * D + r] = mx;
+        cta_part[R * D + R + r] = sum;
       }
     }
   }
@@ -796,11 +749,7 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   const uint32_t full = sm103::smem_u32(&s_full[team][0]);
   const T *q = static_cast<const T *>(p.q);
   const int chunks = (p.group + R - 1) / R, segs = p.n_kv * chunks;
-  if (lane < 2) {
-    s_part.id[lane][team] = -1;
-    s_part.ends[lane][team] = 1;
-    s_part.o[lane][team] = reinterpret_cast<const float *>(my);
-  }
+  if (lane == 0) s_part.state[team] = 0;
   if constexpr (kTma) {
     if (threadIdx.x == 0) {
       sm103::tma_prefetch_map(&maps.k);
@@ -1033,36 +982,41 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
           if ((lane & 3) == 0) write_stats(p, b, n0 + r, m[i] * kLn2, l[i]);
         }
       } else {
-        team_sync<TW>();            // the ring has been read
-        const int slot = opens ? 1 : 0;
-        float *dst = partial_at<NT, TW>(p, R, what & kRangeEnds, my);
+        // To the workspace, or, in a direct call, to shared memory: the ring, whose
+        // last block this was.
+        team_sync<TW>();
+        const int pitch = p.direct ? D + Sh::PAD : D;
+        float *slot = slot_of(p, blockIdx.x * NT + team, opens ? 1 : 0);
+        float *dst = p.direct ? reinterpret_cast<float *>(my) : slot;
+        float *dst_m = p.direct ? s_part.m[team] : slot + p.slot_rows * D;
+        float *dst_l = p.direct ? s_part.l[team] : slot + p.slot_rows * (D + 1);
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
+          if (row + i * 8 >= heads) continue;
           const int r = row0 + row + i * 8;
           if ((lane & 3) == 0) {
-            s_part.m[slot][team][r] = m[i];
-            s_part.l[slot][team][r] = l[i];
+            dst_m[r] = m[i];
+            dst_l[r] = l[i];
           }
 #pragma unroll
           for (int k = 0; k < D / 8; ++k)
-            *reinterpret_cast<float2 *>(dst + r * (D + Sh::PAD) + col + k * 8) =
+            *reinterpret_cast<float2 *>(dst + r * pitch + col + k * 8) =
                 NR == 1 ? make_float2(o[k][0] + o[k][2], o[k][1] + o[k][3])
                        : make_float2(o[k][i * 2], o[k][i * 2 + 1]);
         }
-        if (lane == 0) {
-          s_part.id[slot][team] = id;
-          s_part.ends[slot][team] = ends;
-          s_part.o[slot][team] = dst;
-        }
+        if (lane == 0)
+          s_part.state[team] = kHas | (opens ? kSegBegins : 0) | (ends ? kSegEnds : 0);
       }
     }
   }
-  __syncthreads();
-  float *cta_part = reinterpret_cast<float *>(smem + NT * Sh::kRing);
-  merge_partials<T, D, R, NW, NT, Sh::PAD>(p, chunks, s_part, cta_part);
-  if (p.direct > 1) join_cluster<T, D, R, NW, NT, KB>(p, chunks, cta_part);
+  if (p.direct) {
+    __syncthreads();
+    float *cta_part = reinterpret_cast<float *>(smem + NT * Sh::kRing);
+    merge_cta<T, D, R, Sh>(p, chunks, s_part, smem, cta_part);
+    if (p.direct > 1) join_cluster<T, D, R, NW, NT, KB>(p, chunks, cta_part);
+  }
   if constexpr (kTma) {
-    if (s_abort) {
+    if (*static_cast<volatile int *>(&s_abort)) {
       load.err |= FA_PAGED_TIMEOUT;
       drain(full, S, stage, parity);
     }
@@ -1100,11 +1054,7 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
   float *s_p = reinterpret_cast<float *>(extra + Sh::QS * Sh::kQ);   // weights [8][R]
   float *s_q = nullptr;                                               // the part's query rows
   const int chunks = (p.group + R - 1) / R, segs = p.n_kv * chunks;
-  if (lane < 2) {
-    s_part.id[lane][warp] = -1;
-    s_part.ends[lane][warp] = 1;
-    s_part.o[lane][warp] = reinterpret_cast<const float *>(my);
-  }
+  if (lane == 0) s_part.state[warp] = 0;
 
   const uint32_t full = sm103::smem_u32(&s_full[warp][0]);
   if constexpr (kTma) {
@@ -1254,15 +1204,18 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
         for (int x = 4; x < 32; x <<= 1) l[r] += __shfl_xor_sync(kFull, l[r], x);
       }
       const bool whole = opens && ends;
-      const int slot = opens ? 1 : 0;
       __syncwarp();                  // the ring has been read
-      float *dst = partial_at<NW, 1>(p, R, what & kRangeEnds, my);
+      const int pitch = p.direct ? D + Sh::PAD : D;
+      float *slot = slot_of(p, blockIdx.x * NW + warp, opens ? 1 : 0);
+      float *dst = p.direct ? reinterpret_cast<float *>(my) : slot;
+      float *dst_m = p.direct ? s_part.m[warp] : slot + p.slot_rows * D;
+      float *dst_l = p.direct ? s_part.l[warp] : slot + p.slot_rows * (D + 1);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (r >= heads) continue;
         const float inv = whole ? (l[r] == 0.f ? 0.f : 1.f / l[r]) : 1.f;
         float *to = whole ? static_cast<float *>(p.y) + b * p.y_stride + int64_t(n0 + r) * D
-                          : dst + r * (D + Sh::PAD);
+                          : dst + r * pitch;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -1271,24 +1224,23 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
           if (whole) {
             write_stats(p, b, n0 + r, m[r] * kLn2, l[r]);
           } else {
-            s_part.m[slot][warp][r] = m[r];
-            s_part.l[slot][warp][r] = l[r];
+            dst_m[r] = m[r];
+            dst_l[r] = l[r];
           }
         }
       }
-      if (lane == 0 && !whole) {
-        s_part.id[slot][warp] = id;
-        s_part.ends[slot][warp] = ends;
-        s_part.o[slot][warp] = dst;
-      }
+      if (lane == 0 && !whole)
+        s_part.state[warp] = kHas | (opens ? kSegBegins : 0) | (ends ? kSegEnds : 0);
     }
   }
-  __syncthreads();
-  float *cta_part = reinterpret_cast<float *>(smem + NW * Sh::kRing);
-  merge_partials<float, D, R, NW, NW, Sh::PAD>(p, chunks, s_part, cta_part);
-  if (p.direct > 1) join_cluster<float, D, R, NW, NW, KB>(p, chunks, cta_part);
+  if (p.direct) {
+    __syncthreads();
+    float *cta_part = reinterpret_cast<float *>(smem + NW * Sh::kRing);
+    merge_cta<float, D, R, Sh>(p, chunks, s_part, smem, cta_part);
+    if (p.direct > 1) join_cluster<float, D, R, NW, NW, KB>(p, chunks, cta_part);
+  }
   if constexpr (kTma) {
-    if (s_abort) {
+    if (*static_cast<volatile int *>(&s_abort)) {
       load.err |= FA_PAGED_TIMEOUT;
       drain(full, S, stage, parity);
     }
@@ -1297,24 +1249,22 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
 }
 
 // ---------------------------------------------------------------------------
-// Joins the sums of the segments that were cut between CTAs.  Block (x, r)
-// takes query head r of segment x, or, where there are more segments than
-// CTAs, of the segment in which CTA x's ranges end.  Which CTAs share it
-// follows from the lengths alone, so all that is worked out before the main
-// kernel is done.  The warps take the parts in turn, so that their loads
-// overlap, and meet in shared memory, always in the same order.
+// Adds the parts of the segments that were cut.  Which ranges share a segment
+// follows from the lengths alone, so that is worked out before the main kernel is
+// done.  Block x takes segment x, or, where there are more segments than ranges,
+// the segment in which range x ends.  WPR warps take a query head's parts in turn,
+// so that their loads overlap, and meet in shared memory, always in the same order.
 // ---------------------------------------------------------------------------
-constexpr int kJoinWarps = 8;
-
-template <typename T, int D, int KB, int NT>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(
-    const __grid_constant__ DecodeParams p, int rows, int by_segment) {
+template <typename T, int D, int KB, int WPR>
+__global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256) join_kernel(
+    const __grid_constant__ DecodeParams p, int by_segment) {
   constexpr int PL = D / 32;
-  constexpr int U = 2;               // parts on the way at once, per warp
+  constexpr int kJoinWarps = WPR > 8 ? WPR : 8;
+  constexpr int U = WPR > 8 ? 4 : 2;   // parts on the way at once, per warp
   __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
-  __shared__ float s_o[kJoinWarps][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y;
-  const int chunks = (p.group + rows - 1) / rows, segs = p.n_kv * chunks;
+  __shared__ float s_o[WPR > 1 ? kJoinWarps : 1][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int chunks = (p.group + p.rows - 1) / p.rows, segs = p.n_kv * chunks;
   Line line;
   Place at{0, 0, 0, 1};
   int first_unit;                    // of the segment
@@ -1323,71 +1273,85 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(
     at.seg = blockIdx.x - at.b * segs;
     first_unit = segment_start<KB>(p, segs, at, line);
   } else {
-    const int behind = (blockIdx.x + 1) * NT;
-    find<KB>(p, segs, behind, 1, line, at);
-    first_unit = line.start(behind) - 1 - at.off;
+    find<KB>(p, segs, blockIdx.x + 1, 1, line, at);
+    first_unit = line.start(blockIdx.x + 1) - 1 - at.off;
   }
-  // The CTAs of its first and last block.
-  const int i = line.range_of(first_unit + (kSwitchBlocks >> p.unit_shift)) / NT;
-  const int last = min(line.range_of(first_unit + at.units - 1) / NT, p.grid - 1);
-  const int h = (chunks == 1 ? 0 : at.seg % chunks * rows) + r;
-  const int n = (chunks == 1 ? at.seg : at.seg / chunks) * p.group + h;
+  // The ranges of its first and last block.
+  const int i = line.range_of(first_unit + (kSwitchBlocks >> p.unit_shift));
+  const int last = min(line.range_of(first_unit + at.units - 1), p.ranges - 1);
+  const int hk = chunks == 1 ? at.seg : at.seg / chunks, h0 = (at.seg - hk * chunks) * p.rows;
+  const int rows = min(p.rows, p.group - h0);
 
   // Every block waits, also one with nothing to do: what follows on the stream
   // is behind the main kernel only through this one.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (i == last || h >= p.group || (!by_segment && i != int(blockIdx.x))) return;
-  // Part 0 is CTA i's slot 1, part k CTA (i + k)'s slot 0.
+  if (i >= last || (!by_segment && i != int(blockIdx.x))) return;
   const int parts = last - i + 1;
-  float mx = -CUDART_INF_F, sum = 0.f, acc[PL];
-#pragma unroll
-  for (int k = 0; k < PL; ++k) acc[k] = 0.f;
 #pragma unroll 1
-  for (int j0 = warp; j0 < parts; j0 += U * kJoinWarps) {
-    float m2[U], l2[U], o2[U][PL];
+  for (int r = blockIdx.y * (kJoinWarps / WPR) + warp / WPR; r < rows;
+       r += gridDim.y * (kJoinWarps / WPR)) {
+    // Part 0 is in range i's slot 1, part k in range (i + k)'s slot 0.
+    float mx = -CUDART_INF_F, sum = 0.f, acc[PL];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = min(j0 + u * kJoinWarps, parts - 1);
-      const float *src = slot_of(p, i + j, j == 0 ? 1 : 0, rows);
-      m2[u] = src[rows * D + r];
-      l2[u] = src[rows * D + rows + r];
+    for (int k = 0; k < PL; ++k) acc[k] = 0.f;
+#pragma unroll 1
+    for (int j0 = warp % WPR; j0 < parts; j0 += U * WPR) {
+      float m2[U], l2[U], o2[U][PL];
 #pragma unroll
-      for (int k = 0; k < PL; ++k) o2[u][k] = src[r * D + lane + 32 * k];
+      for (int u = 0; u < U; ++u) {
+        const int j = min(j0 + u * WPR, parts - 1);
+        const float *src = slot_of(p, i + j, j == 0 ? 1 : 0);
+        m2[u] = src[p.slot_rows * D + r];
+        l2[u] = src[p.slot_rows * (D + 1) + r];
+#pragma unroll
+        for (int k = 0; k < PL; ++k) o2[u][k] = src[r * D + lane + 32 * k];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (j0 + u * WPR >= parts) break;
+        const float mn = fmaxf(mx, m2[u]), ref = mn == -CUDART_INF_F ? 0.f : mn;
+        const float f = sm103::ex2(mx - ref), f2 = sm103::ex2(m2[u] - ref);
+        mx = mn;
+        sum = sum * f + l2[u] * f2;
+#pragma unroll
+        for (int k = 0; k < PL; ++k) acc[k] = acc[k] * f + o2[u][k] * f2;
+      }
     }
+    const int n = hk * p.group + h0 + r;
+    T *y = static_cast<T *>(p.y) + at.b * p.y_stride + int64_t(n) * D;
+    if constexpr (WPR == 1) {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (j0 + u * kJoinWarps >= parts) break;
-      const float mn = fmaxf(mx, m2[u]), ref = mn == -CUDART_INF_F ? 0.f : mn;
-      const float f = sm103::ex2(mx - ref), f2 = sm103::ex2(m2[u] - ref);
-      mx = mn;
-      sum = sum * f + l2[u] * f2;
+      for (int k = 0; k < PL; ++k) y[lane + 32 * k] = from_f<T>(acc[k] * inv);
+      if (lane == 0) write_stats(p, at.b, n, mx * kLn2, sum);
+    } else {
+      // All warps are here: WPR is the whole block, and r its row.
+      __syncthreads();
+      if (lane == 0) {
+        s_m[warp] = mx;
+        s_l[warp] = sum;
+      }
 #pragma unroll
-      for (int k = 0; k < PL; ++k) acc[k] = acc[k] * f + o2[u][k] * f2;
+      for (int k = 0; k < PL; ++k) s_o[warp][lane + 32 * k] = acc[k];
+      __syncthreads();
+      const int d = threadIdx.x;
+      if (d < D) {
+        float top = -CUDART_INF_F;
+#pragma unroll
+        for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, s_m[k]);
+        const float ref = top == -CUDART_INF_F ? 0.f : top;
+        float total = 0.f, out = 0.f;
+#pragma unroll
+        for (int k = 0; k < kJoinWarps; ++k) {
+          const float f = sm103::ex2(s_m[k] - ref);
+          total += f * s_l[k];
+          out += f * s_o[k][d];
+        }
+        y[d] = from_f<T>(total == 0.f ? 0.f : out / total);
+        if (d == 0) write_stats(p, at.b, n, top * kLn2, total);
+      }
     }
   }
-  if (lane == 0) {
-    s_m[warp] = mx;
-    s_l[warp] = sum;
-  }
-#pragma unroll
-  for (int k = 0; k < PL; ++k) s_o[warp][lane + 32 * k] = acc[k];
-  __syncthreads();
-  const int d = threadIdx.x;
-  if (d >= D) return;
-  float top = -CUDART_INF_F;
-#pragma unroll
-  for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, s_m[k]);
-  const float ref = top == -CUDART_INF_F ? 0.f : top;
-  float total = 0.f, out = 0.f;
-#pragma unroll
-  for (int k = 0; k < kJoinWarps; ++k) {
-    const float f = sm103::ex2(s_m[k] - ref);
-    total += f * s_l[k];
-    out += f * s_o[k][d];
-  }
-  static_cast<T *>(p.y)[at.b * p.y_stride + int64_t(n) * D + d] =
-      from_f<T>(total == 0.f ? 0.f : out / total);
-  if (d == 0) write_stats(p, at.b, n, top * kLn2, total);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -1486,12 +1450,21 @@ cudaError_t launch_shape(DecodeParams p, Kernel with_tma, Kernel without, int sm
   while (segments * ((blocks >> p.unit_shift) + 1) >= (int64_t(1) << 31)) ++p.unit_shift;
   kernel<<<p.grid, NW * 32, Sh::kSmem, s>>>(p, maps);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int by_segment = segments <= p.grid;
-  cfg.gridDim = dim3(unsigned(by_segment ? segments : p.grid), unsigned(p.group < R ? p.group : R));
-  cfg.blockDim = dim3(kJoinWarps * 32);
+  // 32 warps per query head where a segment has 16 parts and more and two such
+  // blocks per SM suffice (152 parts take 2 us so, 10 us with 8 warps; 1024 heads of
+  // 19 parts take 13 us less with 8); then 8 warps, and one where the GPU does not
+  // hold blocks of those for all heads.
+  const int by_segment = segments <= p.ranges;
+  const int64_t heads = segments * p.slot_rows;
+  const int warps = segments * 16 <= p.ranges && heads <= 2 * sms ? 32 : heads <= 8 * sms ? 8 : 1;
+  cfg.gridDim = dim3(unsigned(by_segment ? segments : p.ranges),
+                     unsigned(warps > 1 ? p.slot_rows : (p.slot_rows + 7) / 8));
+  cfg.blockDim = dim3(warps == 32 ? 1024 : 256);
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<T, D, KB, NT>, p, R, by_segment);
+  return warps == 32  ? cudaLaunchKernelEx(&cfg, join_kernel<T, D, KB, 32>, p, by_segment)
+         : warps == 8 ? cudaLaunchKernelEx(&cfg, join_kernel<T, D, KB, 8>, p, by_segment)
+                      : cudaLaunchKernelEx(&cfg, join_kernel<T, D, KB, 1>, p, by_segment);
 }
 
 template <typename T, int D, int R>
