@@ -416,6 +416,57 @@ enum {
   FA_PAGED_TIMEOUT = 128
 };
 
+/* Arguments, in the order of the descriptions below.  Device pointers except
+ * for the structs themselves; dtype is an fa_dtype, reserved is 0
+ * (FA_ERR_INVALID otherwise). */
+typedef struct {
+  int32_t *block_table;
+  int64_t max_pages, table_stride;
+  const int32_t *seq_lens, *delta;
+  int64_t batch;
+  int32_t *free_pages;
+  const int64_t *free_state;
+  int64_t num_pages, page_size;
+  int64_t *slots;
+  int64_t max_tokens;
+  int64_t *cu_tokens;
+  int32_t *seq_lens_out;
+  int64_t *free_state_out;
+  int32_t *error;
+} fa_paged_plan_args;
+
+typedef struct {
+  const void *k, *v;
+  int64_t k_stride, v_stride;
+  const int64_t *slots;
+  int64_t tokens;
+  void *k_pages, *v_pages;
+  int64_t num_pages, page_size, head_num_kv, head_dim;
+  int64_t page_stride, token_stride, head_stride;
+  int32_t dtype, reserved;
+  int32_t *error;
+} fa_paged_write_args;
+
+typedef struct {
+  const void *q;
+  int64_t q_stride;
+  const void *k_pages, *v_pages;
+  int64_t num_pages, page_size, page_stride, token_stride, head_stride;
+  const int32_t *block_table;
+  int64_t max_pages, table_stride;
+  const int32_t *seq_lens;
+  int64_t batch, head_num, head_num_kv, head_dim;
+  int32_t dtype, reserved;
+  double scale;
+  int64_t pre_tokens;
+  void *y;
+  int64_t y_stride;
+  float *softmax_max, *softmax_sum;
+  int32_t *error;
+  void *workspace;
+  size_t workspace_bytes;
+} fa_paged_decode_args;
+
 /* Grows and shrinks the requests by delta[b] tokens each (device int32
  * [batch]) and maps the new tokens to cache slots.
  *   delta > 0   the request takes that many tokens, and the pages that they
@@ -444,12 +495,7 @@ enum {
  * and of pages given back are written, all others are left as they were (so
  * are the table's entries of pages given back).  No two calls on one pool may
  * overlap.  max_tokens in [0, 2^31); slots may be NULL when it is 0. */
-fa_status fa_paged_plan(int32_t *block_table, int64_t max_pages, int64_t table_stride,
-                        const int32_t *seq_lens, const int32_t *delta, int64_t batch,
-                        int32_t *free_pages, const int64_t *free_state, int64_t num_pages,
-                        int64_t page_size, int64_t *slots, int64_t max_tokens,
-                        int64_t *cu_tokens, int32_t *seq_lens_out, int64_t *free_state_out,
-                        int32_t *error, fa_stream_t stream);
+fa_status fa_paged_plan(const fa_paged_plan_args *args, fa_stream_t stream);
 
 /* Copies row t of k and v ([tokens, head_num_kv, head_dim], rows k_stride /
  * v_stride elements apart, heads contiguous) to cache slot slots[t] =
@@ -458,12 +504,7 @@ fa_status fa_paged_plan(int32_t *block_table, int64_t max_pages, int64_t table_s
  * twice then holds is unspecified.  k and v need no alignment beyond their
  * type's; with 16-byte aligned rows the copies are wider.  tokens in
  * [0, 2^31); tokens == 0 returns FA_OK without a launch. */
-fa_status fa_paged_write(const void *k, const void *v, int64_t k_stride, int64_t v_stride,
-                         const int64_t *slots, int64_t tokens, void *k_pages, void *v_pages,
-                         int64_t num_pages, int64_t page_size, int64_t head_num_kv,
-                         int64_t head_dim, int64_t page_stride, int64_t token_stride,
-                         int64_t head_stride, fa_dtype dtype, int32_t *error,
-                         fa_stream_t stream);
+fa_status fa_paged_write(const fa_paged_write_args *args, fa_stream_t stream);
 
 /* Workspace of fa_paged_decode in bytes (0: it needs none), on the current
  * device, from the same scalars.  It does not depend on the lengths.  A
@@ -489,15 +530,7 @@ fa_status fa_paged_decode_workspace_size(int64_t batch, int64_t head_num, int64_
  * does not change from run to run on one device (fixed add order).
  * workspace: 16-byte aligned (FA_ERR_INVALID otherwise), at least what
  * fa_paged_decode_workspace_size gives; NULL where that is 0. */
-fa_status fa_paged_decode(const void *q, int64_t q_stride, const void *k_pages,
-                          const void *v_pages, int64_t num_pages, int64_t page_size,
-                          int64_t page_stride, int64_t token_stride, int64_t head_stride,
-                          const int32_t *block_table, int64_t max_pages, int64_t table_stride,
-                          const int32_t *seq_lens, int64_t batch, int64_t head_num,
-                          int64_t head_num_kv, int64_t head_dim, fa_dtype dtype, double scale,
-                          int64_t pre_tokens, void *y, int64_t y_stride, float *softmax_max,
-                          float *softmax_sum, int32_t *error, void *workspace,
-                          size_t workspace_bytes, fa_stream_t stream);
+fa_status fa_paged_decode(const fa_paged_decode_args *args, fa_stream_t stream);
 
 /* Library version: major * 10000 + minor * 100 + patch. */
 int32_t fa_varlen_version(void);

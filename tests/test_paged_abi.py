@@ -2,6 +2,8 @@
 refused before anything is launched; the addresses are never read."""
 
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -21,20 +23,50 @@ def built():
 
 PLAN = dict(block_table=P, max_pages=8, table_stride=8, seq_lens=P, delta=P, batch=4, free_pages=P,
             free_state=P, num_pages=64, page_size=16, slots=P, max_tokens=64, cu_tokens=P,
-            seq_lens_out=P, free_state_out=P, error=None, stream=None)
+            seq_lens_out=P, free_state_out=P, error=0)
 WRITE = dict(k=P, v=P, k_stride=512, v_stride=512, slots=P, tokens=4, k_pages=P, v_pages=P,
              num_pages=64, page_size=16, head_num_kv=4, head_dim=128, page_stride=16 * 512,
-             token_stride=512, head_stride=128, dtype=2, error=None, stream=None)
+             token_stride=512, head_stride=128, dtype=2, reserved=0, error=0)
 DECODE = dict(q=P, q_stride=1024, k_pages=P, v_pages=P, num_pages=64, page_size=16,
               page_stride=16 * 512, token_stride=512, head_stride=128, block_table=P, max_pages=8,
               table_stride=8, seq_lens=P, batch=4, head_num=8, head_num_kv=4, head_dim=128, dtype=2,
-              scale=0.1, pre_tokens=BIG, y=P, y_stride=1024, softmax_max=None, softmax_sum=None,
-              error=None, workspace=P, workspace_bytes=0, stream=None)
+              reserved=0, scale=0.1, pre_tokens=BIG, y=P, y_stride=1024, softmax_max=0,
+              softmax_sum=0, error=0, workspace=P, workspace_bytes=0)
 
 
 def call(name, base, **kw):
     assert set(kw) <= set(base)
-    return getattr(fa.lib(), name)(*{**base, **kw}.values())
+    pack = {"fa_paged_plan": fa._pack_plan, "fa_paged_write": fa._pack_write,
+            "fa_paged_decode": fa._pack_decode}[name]
+    args = {k: v or 0 for k, v in {**base, **kw}.items()}
+    return getattr(fa.lib(), name)(pack(*args.values()), None)
+
+
+def test_the_structs_are_packed_as_the_header_lays_them_out():
+    text = open(os.path.join(fb.INCLUDE, "fa_varlen.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    for name, fields, base in (("plan", fa.PLAN_ARGS, PLAN), ("write", fa.WRITE_ARGS, WRITE),
+                               ("decode", fa.DECODE_ARGS, DECODE)):
+        assert list(base) == fields
+        body = re.search(r"typedef struct \{([^}]*)\} fa_paged_%s_args;" % name, text).group(1)
+        found, size = [], 0
+        for declared in filter(None, (d.strip() for d in body.split(";"))):
+            kind, names = re.match(r"(?:const )?(\w+)\s+(.*)", declared, re.S).groups()
+            for field in names.split(","):
+                found.append(field.strip().lstrip("*"))
+                size += 4 if kind == "int32_t" and "*" not in field else 8
+        assert found == fields
+        assert fa._format(fields).size == size
+
+
+@pytest.mark.parametrize("name", ["fa_paged_plan", "fa_paged_write", "fa_paged_decode"])
+def test_no_arguments(name):
+    assert getattr(fa.lib(), name)(None, None) == fa.FA_ERR_NULLPTR
+
+
+def test_reserved_is_zero():
+    assert call("fa_paged_write", WRITE, reserved=1) == fa.FA_ERR_INVALID
+    assert call("fa_paged_decode", DECODE, reserved=7) == fa.FA_ERR_INVALID
 
 
 @pytest.mark.parametrize("null", ["block_table", "seq_lens", "delta", "free_pages", "free_state",

@@ -245,6 +245,15 @@ def test_decode_batches(batch, length):
     run_decode("bf16", lens, 2, 1, 32, 16, seed=batch)
 
 
+@pytest.mark.parametrize("dtype,batch,heads,heads_kv,shortest,page", [
+    ("bf16", 40, 16, 8, 1500, 16), ("fp16", 100, 64, 2, 1600, 24), ("fp32", 20, 8, 8, 1500, 32)])
+def test_decode_large_batches(dtype, batch, heads, heads_kv, shortest, page):
+    # Many blocks in each warp's range, and many segments in some.
+    lens = np.random.default_rng(batch).integers(shortest, 2500, batch)
+    lens[3] = 0
+    run_decode(dtype, lens, heads, heads_kv, 32, page, seed=batch)
+
+
 def test_decode_all_empty():
     for dtype in DTYPE:
         y = run_decode(dtype, [0, 0, 0], 4, 2, 64, 16)

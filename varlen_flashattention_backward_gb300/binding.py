@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 
 import torch
 
@@ -88,13 +89,10 @@ _SIGS = {
     "fa_varlen_bwd_schedule_ex": ([_pi64, _pi64, _i64, _i64, _i64, _i64, _i32, _i64, _i64, _i32,
                                    _i64, _i64, _i32, ctypes.POINTER(ctypes.c_int32), _i64, _pi64],
                                   _i32),
-    "fa_paged_plan": ([_vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp,
-                       _vp, _vp, _vp], _i32),
-    "fa_paged_write": ([_vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp] + [_i64] * 7 +
-                       [_i32, _vp, _vp], _i32),
+    "fa_paged_plan": ([_cp, _vp], _i32),
+    "fa_paged_write": ([_cp, _vp], _i32),
     "fa_paged_decode_workspace_size": ([_i64] * 4 + [_i32] + [_i64] * 3 + [_psz], _i32),
-    "fa_paged_decode": ([_vp, _i64, _vp, _vp] + [_i64] * 5 + [_vp, _i64, _i64, _vp] + [_i64] * 4 +
-                        [_i32, _f64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "fa_paged_decode": ([_cp, _vp], _i32),
 }
 
 EXPORTS = tuple(_SIGS)
@@ -387,9 +385,31 @@ def gen_keep_mask(nbits: int, seed: int, keep_prob: float, device="cuda", out=No
 # Paged key/value cache
 # ---------------------------------------------------------------------------
 
-# A decoding step makes these calls for every layer, so what they check is
-# arranged to cost little: one expression of integer comparisons per tensor,
-# and the sentence that explains a refusal is only put together for one.
+# A decoding step makes these calls for every layer, so they are arranged to cost
+# little: the argument structs are packed in one go, the checks are one expression
+# of integer comparisons per tensor, and the sentence that explains a refusal is
+# only put together for one.
+
+# Fields of the C structs, in order: q a 64-bit number or address, d a double, i
+# a 32-bit number.
+PLAN_ARGS = ("block_table max_pages table_stride seq_lens delta batch free_pages free_state num_pages "
+             "page_size slots max_tokens cu_tokens seq_lens_out free_state_out error").split()
+WRITE_ARGS = ("k v k_stride v_stride slots tokens k_pages v_pages num_pages page_size head_num_kv "
+              "head_dim page_stride token_stride head_stride dtype reserved error").split()
+DECODE_ARGS = ("q q_stride k_pages v_pages num_pages page_size page_stride token_stride head_stride "
+               "block_table max_pages table_stride seq_lens batch head_num head_num_kv head_dim dtype "
+               "reserved scale pre_tokens y y_stride softmax_max softmax_sum error workspace "
+               "workspace_bytes").split()
+
+
+def _format(names):
+    kinds = {"dtype": "i", "reserved": "i", "scale": "d"}
+    return struct.Struct("@" + "".join(kinds.get(n, "q") for n in names))
+
+
+_pack_plan, _pack_write, _pack_decode = (_format(n).pack
+                                         for n in (PLAN_ARGS, WRITE_ARGS, DECODE_ARGS))
+
 
 class _On:
     """Makes `stream` (or, without one, the current stream of device `index`)
@@ -474,6 +494,14 @@ def _rows(t, rows, heads, dim, dtype, index, name):
     return stride[0]
 
 
+def _lanes(t, b, n, index, name):
+    """A contiguous tensor of statistics."""
+    if not (t.shape == (b, n, 8) and t.dtype is torch.float32 and t.is_contiguous() and
+            t.get_device() == index):
+        _refuse(name, t, f"contiguous fp32 {(b, n, 8)}", index)
+    return t.data_ptr()
+
+
 def paged_plan(block_table, seq_lens, delta, free_pages, free_state, page_size, max_tokens,
                slots=None, cu_tokens=None, seq_lens_out=None, free_state_out=None, error=None,
                stream=None):
@@ -511,13 +539,13 @@ def paged_plan(block_table, seq_lens, delta, free_pages, free_state, page_size, 
         at_state = free_state_out.data_ptr()
     else:
         at_state = _flat(free_state_out, i64, 2, index, "free_state_out")
-    status = (_LIB or lib()).fa_paged_plan(
+    status = (_LIB or lib()).fa_paged_plan(_pack_plan(
         block_table.data_ptr(), max_pages, stride, _flat(seq_lens, i32, b, index, "seq_lens"),
         _flat(delta, i32, b, index, "delta"), b,
         _flat(free_pages, i32, pages, index, "free_pages"),
         _flat(free_state, i64, 2, index, "free_state"), pages, int(page_size), at_slots,
         max_tokens, at_cu, at_lens, at_state,
-        None if error is None else _flat(error, i32, 1, index, "error"), _raw_stream(index))
+        0 if error is None else _flat(error, i32, 1, index, "error")), _raw_stream(index))
     if status:
         _check(status, "fa_paged_plan")
     return slots, cu_tokens, seq_lens_out, free_state_out
@@ -533,12 +561,12 @@ def paged_write(k, v, slots, k_pages, v_pages, error=None, stream=None):
             return paged_write(k, v, slots, k_pages, v_pages, error)
     shape, strides = _pages(k_pages, v_pages, index)
     tokens, dtype = slots.numel(), k_pages.dtype
-    status = (_LIB or lib()).fa_paged_write(
+    status = (_LIB or lib()).fa_paged_write(_pack_write(
         k.data_ptr(), v.data_ptr(), _rows(k, tokens, shape[2], shape[3], dtype, index, "k"),
         _rows(v, tokens, shape[2], shape[3], dtype, index, "v"),
         _flat(slots, torch.int64, tokens, index, "slots"), tokens, k_pages.data_ptr(),
-        v_pages.data_ptr(), *shape, strides[0], strides[1], strides[2], _DTYPE[dtype],
-        None if error is None else _flat(error, torch.int32, 1, index, "error"),
+        v_pages.data_ptr(), *shape, strides[0], strides[1], strides[2], _DTYPE[dtype], 0,
+        0 if error is None else _flat(error, torch.int32, 1, index, "error")),
         _raw_stream(index))
     if status:
         _check(status, "fa_paged_write")
@@ -584,18 +612,19 @@ def paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, pre_tokens=2
         y, ys = torch.empty((b, n, d), dtype=dtype, device=dev), n * d
     else:
         ys = _rows(y, b, n, d, dtype, index, "y")
-    top = total = None
+    top = total = 0
     if stats or softmax_max is not None or softmax_sum is not None:
         if softmax_max is None:
             softmax_max = torch.empty((b, n, 8), dtype=torch.float32, device=dev)
+            top = softmax_max.data_ptr()
+        else:
+            top = _lanes(softmax_max, b, n, index, "softmax_max")
         if softmax_sum is None:
             softmax_sum = torch.empty((b, n, 8), dtype=torch.float32, device=dev)
-        for name, t in (("softmax_max", softmax_max), ("softmax_sum", softmax_sum)):
-            if not (t.shape == (b, n, 8) and t.dtype is torch.float32 and t.is_contiguous() and
-                    t.get_device() == index):
-                _refuse(name, t, f"contiguous fp32 {(b, n, 8)}", index)
-        top, total = softmax_max.data_ptr(), softmax_sum.data_ptr()
-    at_workspace = None
+            total = softmax_sum.data_ptr()
+        else:
+            total = _lanes(softmax_sum, b, n, index, "softmax_sum")
+    at_workspace = 0
     if workspace is None:
         nbytes = _decode_workspace(index, b, n, n_kv, d, dtype, shape[1], max_pages, pre_tokens)
         if nbytes:
@@ -606,13 +635,13 @@ def paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, pre_tokens=2
         if not (workspace.is_contiguous() and workspace.get_device() == index):
             _refuse("workspace", workspace, "contiguous memory", index)
         at_workspace = workspace.data_ptr()
-    status = (_LIB or lib()).fa_paged_decode(
+    status = (_LIB or lib()).fa_paged_decode(_pack_decode(
         q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), shape[0], shape[1], strides[0],
         strides[1], strides[2], block_table.data_ptr(), max_pages, table_stride,
-        _flat(seq_lens, torch.int32, b, index, "seq_lens"), b, n, n_kv, d, _DTYPE[dtype], scale,
+        _flat(seq_lens, torch.int32, b, index, "seq_lens"), b, n, n_kv, d, _DTYPE[dtype], 0, scale,
         min(max(int(pre_tokens), -1), 2 ** 40), y.data_ptr(), ys, top, total,
-        None if error is None else _flat(error, torch.int32, 1, index, "error"),
-        at_workspace, nbytes, _raw_stream(index))
+        0 if error is None else _flat(error, torch.int32, 1, index, "error"), at_workspace,
+        nbytes), _raw_stream(index))
     if status:
         _check(status, "fa_paged_decode")
     return y, softmax_max, softmax_sum

@@ -120,77 +120,81 @@ using namespace fav;
 
 extern "C" {
 
-fa_status fa_paged_plan(int32_t *block_table, int64_t max_pages, int64_t table_stride,
-                        const int32_t *seq_lens, const int32_t *delta, int64_t batch,
-                        int32_t *free_pages, const int64_t *free_state, int64_t num_pages,
-                        int64_t page_size, int64_t *slots, int64_t max_tokens,
-                        int64_t *cu_tokens, int32_t *seq_lens_out, int64_t *free_state_out,
-                        int32_t *error, fa_stream_t stream) {
-  if (!block_table || !seq_lens || !delta || !free_pages || !free_state || !cu_tokens ||
-      !seq_lens_out || !free_state_out || (max_tokens > 0 && !slots))
+fa_status fa_paged_plan(const fa_paged_plan_args *args, fa_stream_t stream) {
+  if (!args) return FA_ERR_NULLPTR;
+  const auto &a = *args;
+  if (!a.block_table || !a.seq_lens || !a.delta || !a.free_pages || !a.free_state ||
+      !a.cu_tokens || !a.seq_lens_out || !a.free_state_out || (a.max_tokens > 0 && !a.slots))
     return FA_ERR_NULLPTR;
-  const fa_status st = check_table(batch, num_pages, page_size, max_pages, table_stride);
+  const fa_status st =
+      check_table(a.batch, a.num_pages, a.page_size, a.max_pages, a.table_stride);
   if (st != FA_OK) return st;
-  if (max_tokens < 0 || max_tokens > kMaxI32) return FA_ERR_INVALID;
+  if (a.max_tokens < 0 || a.max_tokens > kMaxI32) return FA_ERR_INVALID;
   PlanParams p{};
-  p.table = block_table;
-  p.table_stride = table_stride;
-  p.lens = seq_lens;
-  p.delta = delta;
-  p.ring = free_pages;
-  p.state = free_state;
-  p.slots = slots;
-  p.cu = cu_tokens;
-  p.lens_out = seq_lens_out;
-  p.state_out = free_state_out;
-  p.error = error;
-  p.max_tokens = max_tokens;
-  p.batch = int(batch);
-  p.max_pages = int(max_pages);
-  p.num_pages = int(num_pages);
-  p.page_size = int(page_size);
-  p.page_shift = log2_or_none(page_size);
+  p.table = a.block_table;
+  p.table_stride = a.table_stride;
+  p.lens = a.seq_lens;
+  p.delta = a.delta;
+  p.ring = a.free_pages;
+  p.state = a.free_state;
+  p.slots = a.slots;
+  p.cu = a.cu_tokens;
+  p.lens_out = a.seq_lens_out;
+  p.state_out = a.free_state_out;
+  p.error = a.error;
+  p.max_tokens = a.max_tokens;
+  p.batch = int(a.batch);
+  p.max_pages = int(a.max_pages);
+  p.num_pages = int(a.num_pages);
+  p.page_size = int(a.page_size);
+  p.page_shift = log2_or_none(a.page_size);
   return launch_paged_plan(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
                                                                                      : FA_ERR_CUDA;
 }
 
-fa_status fa_paged_write(const void *k, const void *v, int64_t k_stride, int64_t v_stride,
-                         const int64_t *slots, int64_t tokens, void *k_pages, void *v_pages,
-                         int64_t num_pages, int64_t page_size, int64_t head_num_kv,
-                         int64_t head_dim, int64_t page_stride, int64_t token_stride,
-                         int64_t head_stride, fa_dtype dtype, int32_t *error,
-                         fa_stream_t stream) {
-  if (!k_pages || !v_pages || (tokens > 0 && (!k || !v || !slots))) return FA_ERR_NULLPTR;
-  fa_status st = check_heads(head_num_kv, head_num_kv, head_dim, dtype);
+fa_status fa_paged_write(const fa_paged_write_args *args, fa_stream_t stream) {
+  if (!args) return FA_ERR_NULLPTR;
+  const auto &a = *args;
+  if (a.reserved != 0) return FA_ERR_INVALID;
+  int64_t k_stride = a.k_stride;
+  int64_t v_stride = a.v_stride;
+  int64_t page_stride = a.page_stride;
+  int64_t token_stride = a.token_stride;
+  int64_t head_stride = a.head_stride;
+  const fa_dtype dtype = static_cast<fa_dtype>(a.dtype);
+  if (!a.k_pages || !a.v_pages || (a.tokens > 0 && (!a.k || !a.v || !a.slots)))
+    return FA_ERR_NULLPTR;
+  fa_status st = check_heads(a.head_num_kv, a.head_num_kv, a.head_dim, dtype);
   if (st != FA_OK) return st;
-  st = check_table(1, num_pages, page_size, 1, 1);
+  st = check_table(1, a.num_pages, a.page_size, 1, 1);
   if (st != FA_OK) return st;
-  st = check_cache(k_pages, v_pages, num_pages, page_size, head_num_kv, head_dim, page_stride,
-                   token_stride, head_stride, dtype);
+  st = check_cache(a.k_pages, a.v_pages, a.num_pages, a.page_size, a.head_num_kv, a.head_dim,
+                   page_stride, token_stride, head_stride, dtype);
   if (st != FA_OK) return st;
-  if (tokens < 0 || tokens > kMaxI32) return FA_ERR_INVALID;
-  const int64_t row = head_num_kv * head_dim;
-  if (bad_rows(k_stride, tokens, row) || bad_rows(v_stride, tokens, row)) return FA_ERR_INVALID;
-  if (!element_aligned(k, dtype) || !element_aligned(v, dtype)) return FA_ERR_INVALID;
-  if (tokens == 0) return FA_OK;
+  if (a.tokens < 0 || a.tokens > kMaxI32) return FA_ERR_INVALID;
+  const int64_t row = a.head_num_kv * a.head_dim;
+  if (bad_rows(k_stride, a.tokens, row) || bad_rows(v_stride, a.tokens, row))
+    return FA_ERR_INVALID;
+  if (!element_aligned(a.k, dtype) || !element_aligned(a.v, dtype)) return FA_ERR_INVALID;
+  if (a.tokens == 0) return FA_OK;
   WriteParams p{};
-  p.k = k;
-  p.v = v;
+  p.k = a.k;
+  p.v = a.v;
   p.k_stride = k_stride;
   p.v_stride = v_stride;
-  p.slots = slots;
-  p.kc = k_pages;
-  p.vc = v_pages;
-  p.n_slots = num_pages * page_size;
+  p.slots = a.slots;
+  p.kc = a.k_pages;
+  p.vc = a.v_pages;
+  p.n_slots = a.num_pages * a.page_size;
   p.page_stride = page_stride;
   p.token_stride = token_stride;
   p.head_stride = head_stride;
-  p.error = error;
-  p.tokens = int(tokens);
-  p.page_size = int(page_size);
-  p.page_shift = log2_or_none(page_size);
-  p.n_kv = int(head_num_kv);
-  p.d = int(head_dim);
+  p.error = a.error;
+  p.tokens = int(a.tokens);
+  p.page_size = int(a.page_size);
+  p.page_shift = log2_or_none(a.page_size);
+  p.n_kv = int(a.head_num_kv);
+  p.d = int(a.head_dim);
   return launch_paged_write(p, dtype, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
@@ -213,77 +217,79 @@ fa_status fa_paged_decode_workspace_size(int64_t batch, int64_t head_num, int64_
   return FA_OK;
 }
 
-fa_status fa_paged_decode(const void *q, int64_t q_stride, const void *k_pages,
-                          const void *v_pages, int64_t num_pages, int64_t page_size,
-                          int64_t page_stride, int64_t token_stride, int64_t head_stride,
-                          const int32_t *block_table, int64_t max_pages, int64_t table_stride,
-                          const int32_t *seq_lens, int64_t batch, int64_t head_num,
-                          int64_t head_num_kv, int64_t head_dim, fa_dtype dtype, double scale,
-                          int64_t pre_tokens, void *y, int64_t y_stride, float *softmax_max,
-                          float *softmax_sum, int32_t *error, void *workspace,
-                          size_t workspace_bytes, fa_stream_t stream) {
-  if (!q || !k_pages || !v_pages || !block_table || !seq_lens || !y ||
-      (!softmax_max != !softmax_sum))
+fa_status fa_paged_decode(const fa_paged_decode_args *args, fa_stream_t stream) {
+  if (!args) return FA_ERR_NULLPTR;
+  const auto &a = *args;
+  if (a.reserved != 0) return FA_ERR_INVALID;
+  int64_t q_stride = a.q_stride;
+  int64_t page_stride = a.page_stride;
+  int64_t token_stride = a.token_stride;
+  int64_t head_stride = a.head_stride;
+  int64_t y_stride = a.y_stride;
+  const fa_dtype dtype = static_cast<fa_dtype>(a.dtype);
+  if (!a.q || !a.k_pages || !a.v_pages || !a.block_table || !a.seq_lens || !a.y ||
+      (!a.softmax_max != !a.softmax_sum))
     return FA_ERR_NULLPTR;
-  fa_status st = check_heads(head_num, head_num_kv, head_dim, dtype);
+  fa_status st = check_heads(a.head_num, a.head_num_kv, a.head_dim, dtype);
   if (st != FA_OK) return st;
-  st = check_table(batch, num_pages, page_size, max_pages, table_stride);
+  st = check_table(a.batch, a.num_pages, a.page_size, a.max_pages, a.table_stride);
   if (st != FA_OK) return st;
-  st = check_cache(k_pages, v_pages, num_pages, page_size, head_num_kv, head_dim, page_stride,
-                   token_stride, head_stride, dtype);
+  st = check_cache(a.k_pages, a.v_pages, a.num_pages, a.page_size, a.head_num_kv, a.head_dim,
+                   page_stride, token_stride, head_stride, dtype);
   if (st != FA_OK) return st;
-  if (!std::isfinite(scale)) return FA_ERR_INVALID;
-  const int64_t row = head_num * head_dim;
-  if (bad_rows(q_stride, batch, row) || bad_rows(y_stride, batch, row)) return FA_ERR_INVALID;
-  if (!element_aligned(q, dtype) || !element_aligned(y, dtype)) return FA_ERR_INVALID;
+  if (!std::isfinite(a.scale)) return FA_ERR_INVALID;
+  const int64_t row = a.head_num * a.head_dim;
+  if (bad_rows(q_stride, a.batch, row) || bad_rows(y_stride, a.batch, row))
+    return FA_ERR_INVALID;
+  if (!element_aligned(a.q, dtype) || !element_aligned(a.y, dtype)) return FA_ERR_INVALID;
   const int sms = sm_count();
-  const int group = int(head_num / head_num_kv);
+  const int group = int(a.head_num / a.head_num_kv);
   const DecodePlan plan =
-      decode_plan(dtype, int(batch), int(head_num_kv), group, int(head_dim),
-                  most_keys(max_pages, page_size, pre_tokens), sms);
-  const size_t bytes = decode_bytes(plan, sms, group, head_dim);
-  if (bytes > 0 && !workspace) return FA_ERR_NULLPTR;
-  if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return FA_ERR_INVALID;
-  if (workspace_bytes < bytes) return FA_ERR_WORKSPACE;
+      decode_plan(dtype, int(a.batch), int(a.head_num_kv), group, int(a.head_dim),
+                  most_keys(a.max_pages, a.page_size, a.pre_tokens), sms);
+  const size_t bytes = decode_bytes(plan, sms, group, a.head_dim);
+  if (bytes > 0 && !a.workspace) return FA_ERR_NULLPTR;
+  if (reinterpret_cast<uintptr_t>(a.workspace) % 16 != 0) return FA_ERR_INVALID;
+  if (a.workspace_bytes < bytes) return FA_ERR_WORKSPACE;
 
   DecodeParams p{};
-  p.q = q;
+  p.q = a.q;
   p.q_stride = q_stride;
-  p.kc = k_pages;
-  p.vc = v_pages;
+  p.kc = a.k_pages;
+  p.vc = a.v_pages;
   p.page_stride = page_stride;
   p.token_stride = token_stride;
   p.head_stride = head_stride;
-  p.table = block_table;
-  p.table_stride = table_stride;
-  p.lens = seq_lens;
-  p.y = y;
+  p.table = a.block_table;
+  p.table_stride = a.table_stride;
+  p.lens = a.seq_lens;
+  p.y = a.y;
   p.y_stride = y_stride;
-  p.smax = softmax_max;
-  p.ssum = softmax_sum;
-  p.error = error;
-  p.part = static_cast<float *>(workspace);
+  p.smax = a.softmax_max;
+  p.ssum = a.softmax_sum;
+  p.error = a.error;
+  p.part = static_cast<float *>(a.workspace);
   p.slot_rows = group < plan.rows ? group : plan.rows;
-  p.num_pages = int(num_pages);
-  p.page_size = int(page_size);
-  p.page_shift = log2_or_none(page_size);
-  p.max_pages = int(max_pages);
-  p.batch = int(batch);
-  p.n = int(head_num);
-  p.n_kv = int(head_num_kv);
-  p.d = int(head_dim);
+  p.num_pages = int(a.num_pages);
+  p.page_size = int(a.page_size);
+  p.page_shift = log2_or_none(a.page_size);
+  p.max_pages = int(a.max_pages);
+  p.batch = int(a.batch);
+  p.n = int(a.head_num);
+  p.n_kv = int(a.head_num_kv);
+  p.d = int(a.head_dim);
   p.group = group;
   p.rows = plan.rows;
   p.direct = plan.direct;
   const auto pairs = [](const void *ptr, int64_t stride) {
     return reinterpret_cast<uintptr_t>(ptr) % 4 == 0 && stride % 2 == 0;
   };
-  p.q_chunks = reinterpret_cast<uintptr_t>(q) % 16 == 0 &&
+  p.q_chunks = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 &&
                q_stride % (dtype == FA_DTYPE_FP32 ? 4 : 8) == 0;
-  p.y_pairs = pairs(y, y_stride);
-  p.pre = int(pre_tokens < -1 ? -1 : pre_tokens > kMaxKeys ? kMaxKeys : pre_tokens);
-  p.scale = float(scale);
-  p.scale_log2 = float(scale * 1.4426950408889634);
+  p.y_pairs = pairs(a.y, y_stride);
+  p.pre = int(a.pre_tokens < -1 ? -1 : a.pre_tokens > kMaxKeys ? kMaxKeys : a.pre_tokens);
+  p.scale = float(a.scale);
+  p.scale_log2 = float(a.scale * 1.4426950408889634);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == FA_DTYPE_FP32   ? launch_paged_decode_fp32(p, sms, cs)
                         : dtype == FA_DTYPE_FP16 ? launch_paged_decode_fp16(p, sms, cs)

@@ -192,9 +192,8 @@ enum : int {
   kPartEnds = 1 << 17,
   kSegBegins = 1 << 18,    // first block of a segment
   kSegEnds = 1 << 19,
-  kRangeEnds = 1 << 20,    // last block of the warp's range
-  kDone = 1 << 21,         // no block: the range is done
-  kRowsFetched = 1 << 22   // the part's query rows are in the place of its turn
+  kDone = 1 << 20,         // no block: the range is done
+  kRowsFetched = 1 << 21   // the part's query rows are in the place of its turn
 };
 
 // Shared memory of one kernel of NW warps: a ring of S stages (K and V block
@@ -409,7 +408,7 @@ struct Loader {
       if (n_hi > n_lo) what |= (kAll >> (KB - n_hi)) & ~((1 << n_lo) - 1);
     }
     if (++blk >= end)
-      what |= kPartEnds | (end == span.blocks ? kSegEnds : 0) | (left == 0 ? kRangeEnds : 0);
+      what |= kPartEnds | (end == span.blocks ? kSegEnds : 0);
     if constexpr (!kTma) {
       if ((what >> (lane % KB)) & 1) {
         const int j = row + lane % KB, idx = page_index(j);
