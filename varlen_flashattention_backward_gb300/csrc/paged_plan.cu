@@ -11,27 +11,38 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxPer = 4;                        // requests per thread
 constexpr int kMaxRequests = kThreads * kMaxPer;  // the largest batch
 
-// Exclusive prefix of v over the CTA's threads; `total` gets the sum.  `buf`
-// holds kWarps values and is not written again before the next barrier.
-__device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t *buf, int64_t &total) {
+// Exclusive prefixes of N values over the CTA's threads; `total` gets the sums.
+// `buf` is not written again before the next barrier.
+template <int N>
+__device__ __forceinline__ void block_prefix(int64_t (&v)[N], int64_t (*buf)[kWarps],
+                                             int64_t (&total)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t x = v;
+  int64_t x[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) x[k] = v[k];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(kFull, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) buf[warp] = x;
-  __syncthreads();
-  int64_t before = x - v;
-  total = 0;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    const int64_t w = buf[i];
-    if (i < warp) before += w;
-    total += w;
+    for (int k = 0; k < N; ++k) {
+      const int64_t y = __shfl_up_sync(kFull, x[k], o);
+      if (lane >= o) x[k] += y;
+    }
   }
-  return before;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (lane == 31) buf[k][warp] = x[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    v[k] = x[k] - v[k];
+    total[k] = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const int64_t w = buf[k][i];
+      if (i < warp) v[k] += w;
+      total[k] += w;
+    }
+  }
 }
 
 // What the flat loops read of each request.
@@ -83,21 +94,23 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(const __grid_constant
 
   int len[kMaxPer], delta[kMaxPer];
   const int64_t head = p.state[0], count = p.state[1];
-  int64_t rows = 0;
+  int64_t rows[1] = {0};
 #pragma unroll
   for (int i = 0; i < kMaxPer; ++i) {
     const int b = tid * per + i;
     const bool in = i < per && b < p.batch;
     len[i] = in ? p.lens[b] : 0;
     delta[i] = in ? p.delta[b] : 0;
-    rows += max(delta[i], 0);
+    rows[0] += max(delta[i], 0);
   }
-  int64_t total_rows, total_need, total_give;
-  int64_t row = block_prefix(rows, buf[0], total_rows);
+  int64_t sums[1], moved_sums[2];
+  block_prefix(rows, &buf[0], sums);
+  int64_t row = rows[0];
+  const int64_t total_rows = sums[0];
 
   int need[kMaxPer], give[kMaxPer], target[kMaxPer], have[kMaxPer];
   bool ask[kMaxPer];
-  int64_t first_row[kMaxPer], needs = 0, gives = 0;
+  int64_t first_row[kMaxPer], moved[2] = {0, 0};   // pages needed, given back
 #pragma unroll
   for (int i = 0; i < kMaxPer; ++i) {
     const bool sound = len[i] >= 0 && len[i] <= most;
@@ -115,11 +128,12 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(const __grid_constant
     const int want = (target[i] + p.page_size - 1) / p.page_size;
     need[i] = ask[i] ? want - have[i] : 0;
     give[i] = sound && delta[i] < 0 ? have[i] - want : 0;
-    needs += need[i];
-    gives += give[i];
+    moved[0] += need[i];
+    moved[1] += give[i];
   }
-  int64_t off_need = block_prefix(needs, buf[1], total_need);
-  int64_t off_give = block_prefix(gives, buf[2], total_give);
+  block_prefix(moved, &buf[1], moved_sums);
+  int64_t off_need = moved[0], off_give = moved[1];
+  const int64_t total_give = moved_sums[1];
   // With room for all of them behind the end, the pages given back land on no
   // entry that this call takes.
   const bool whole = head >= 0 && head < p.num_pages && count >= 0 && count <= p.num_pages &&
