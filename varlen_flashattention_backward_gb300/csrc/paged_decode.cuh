@@ -19,9 +19,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kFull = 0xffffffffu;
 // Beginning a segment costs a warp about as much as this many blocks of keys.
 constexpr int kSwitchBlocks = 1;
-// Most CTAs of a cluster that shares a segment, and blocks for each team of it.
+// Most CTAs of a cluster that shares a segment, and blocks for each team of it (16
+// requests of 512 keys, 8 key heads: 8.7 us so, 13.0 by ranges).
 constexpr int kMaxDirect = 8;
-constexpr int kDirectBlocks = 4;
+constexpr int kDirectBlocks = 8;
 
 // ---------------------------------------------------------------------------
 // Division of the work

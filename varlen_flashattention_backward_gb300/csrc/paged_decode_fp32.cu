@@ -49,14 +49,20 @@ DecodePlan decode_plan(fa_dtype dt, int batch, int n_kv, int group, int d, int64
     plan.rows = group <= 1 ? 1 : group <= 2 ? 2 : group <= 4 ? 4 : 8;
   plan.teams = teams_of(tc, plan.rows, d);
   // The largest cluster per segment that still puts all of them on the GPU at
-  // once, if its teams get at most kDirectBlocks blocks each.
+  // once, if its teams get at most kDirectBlocks blocks each.  Clusters share a
+  // GPC, so fewer large ones fit than SMs would hold (152 SMs: 15 of eight, 36 of
+  // four, 76 of two); a second wave doubles the time.
   const int kb = tc ? 16 : 8;
   const int64_t blocks = (max_keys + kb - 1) / kb + 1;
   const int64_t segments = int64_t(batch) * n_kv * ((group + plan.rows - 1) / plan.rows);
+  const auto fits = [&](int ctas) {
+    const int percent = ctas == 1 ? 100 : ctas == 2 ? 95 : ctas == 4 ? 85 : 63;
+    return segments * ctas * 100 <= int64_t(sms) * percent;
+  };
   int ctas = 1;
-  while (ctas < kMaxDirect && segments * ctas * 2 <= sms && ctas * plan.teams < blocks) ctas *= 2;
+  while (ctas < kMaxDirect && fits(ctas * 2) && ctas * plan.teams < blocks) ctas *= 2;
   plan.direct =
-      segments * ctas <= sms && blocks <= int64_t(ctas) * plan.teams * kDirectBlocks ? ctas : 0;
+      fits(ctas) && blocks <= int64_t(ctas) * plan.teams * kDirectBlocks ? ctas : 0;
   return plan;
 }
 
