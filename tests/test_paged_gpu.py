@@ -402,6 +402,39 @@ def test_two_streams_at_once():
         assert torch.equal(ya, outs[0][0]) and torch.equal(yb, outs[0][1])
 
 
+def test_steps_on_a_stream_without_a_graph():
+    """Plan, write and decode launched one behind the other, where each may
+    start before the one before it is done: every step sees its own lengths, and
+    the cut and joined requests too."""
+    torch.manual_seed(3)
+    heads, heads_kv, dim, page, b, steps = 8, 2, 64, 16, 3, 60
+    n_pages, width = 700, 2600          # a wide table: ranges and a join
+    first = [4000, 17, 2000]
+    kc, vc = (torch.randn(n_pages, page, heads_kv, dim, dtype=torch.bfloat16, device=DEV)
+              for _ in range(2))
+    table = torch.full((b, width), -1, dtype=torch.int32, device=DEV)
+    lens = torch.zeros(b, dtype=torch.int32, device=DEV)
+    ring = torch.arange(n_pages, dtype=torch.int32, device=DEV)
+    state = torch.tensor([0, n_pages], dtype=torch.int64, device=DEV)
+    pool = dict(seq_lens_out=lens, free_state_out=state)
+    fa.paged_plan(table, lens, dev(first, torch.int32), ring, state, page, sum(first), **pool)
+    ones = torch.ones(b, dtype=torch.int32, device=DEV)
+    q = torch.randn(steps, b, heads, dim, dtype=torch.bfloat16, device=DEV)
+    k, v = (torch.randn(steps, b, heads_kv, dim, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    torch.cuda.synchronize()
+    got = []
+    for i in range(steps):
+        slots, _, _, _ = fa.paged_plan(table, lens, ones, ring, state, page, b, **pool)
+        fa.paged_write(k[i], v[i], slots, kc, vc)
+        got.append(fa.paged_decode(q[i], kc, vc, table, lens, 0.125, stats=True))
+    torch.cuda.synchronize()
+    kh, vh, th = f64(kc), f64(vc), table.cpu().numpy()
+    v_max = float(np.abs(vh).max())
+    for i in (0, 1, 15, 16, 31, steps - 1):
+        ref = oracle.paged_decode(f64(q[i]), kh, vh, th, np.array(first) + i + 1, 0.125)
+        check_decode(ref, v_max, dim, "bf16", *got[i])
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_prompt_then_steps_equal_the_packed_forward(dtype):
     """Prompts through plan and write, then decoding steps (plan, write,

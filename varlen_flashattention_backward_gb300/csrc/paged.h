@@ -55,8 +55,7 @@ struct DecodeParams {
   int q_chunks;           // rows of q start on 16-byte boundaries
   int pre;            // pre_tokens clamped to [-1, 2^30]
   int rows, direct;   // DecodePlan
-  int grid;           // CTAs of the main kernel
-  int ranges;         // its teams
+  int ranges;         // teams of the main kernel
   int unit_shift;     // log2 of the blocks in a unit of work
   float scale, scale_log2;
 };

@@ -740,7 +740,6 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   __shared__ Partials<NT, R> s_part;
   __shared__ uint64_t s_full[NT][S];
   __shared__ int s_abort;
-  asm volatile("griddepcontrol.launch_dependents;");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / TW;
   const int row0 = warp % TW * RW;  // first row of the team's that is the warp's
   uint8_t *my = smem + team * Sh::kRing;
@@ -761,6 +760,11 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
     __syncthreads();
   }
 
+  // Launched while the kernel before on the stream may still run: nothing in
+  // memory is read or written before this.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The join reads the lengths as soon as it runs, so it may not before this.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Loader<T, D, Sh, RW, TW, KB, kTma> load(p, maps, chunks);
   load.look();
 #pragma unroll 1
@@ -1046,7 +1050,6 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
   __shared__ Partials<NW, R> s_part;
   __shared__ uint64_t s_full[NW][S];
   __shared__ int s_abort;
-  asm volatile("griddepcontrol.launch_dependents;");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint8_t *my = smem + warp * Sh::kRing;
   uint8_t *extra = smem + NW * Sh::kRing + warp * Sh::kWarpExtra;
@@ -1068,6 +1071,8 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
     __syncthreads();
   }
 
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // as above
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Loader<float, D, Sh, R, 1, KB, kTma> load(p, maps, chunks);
   load.look();
 #pragma unroll 1
@@ -1282,6 +1287,7 @@ __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256) join_kernel(
   const int hk = chunks == 1 ? at.seg : at.seg / chunks, h0 = (at.seg - hk * chunks) * p.rows;
   const int rows = min(p.rows, p.group - h0);
 
+  asm volatile("griddepcontrol.launch_dependents;");
   // Every block waits, also one with nothing to do: what follows on the stream
   // is behind the main kernel only through this one.
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1429,27 +1435,34 @@ cudaError_t launch_shape(DecodeParams p, Kernel with_tma, Kernel without, int sm
   cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
   if (e != cudaSuccess) return e;
+  // Both kernels may be launched before the one before them is done, and wait for
+  // it themselves.  A captured main kernel is not: what precedes it in a graph may
+  // be no kernel.
+  cudaLaunchAttribute attrs[2] = {};
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if ((e = cudaStreamIsCapturing(s, &capture)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr{};
   cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.blockDim = dim3(NW * 32);
+  cfg.dynamicSmemBytes = Sh::kSmem;
+  cfg.attrs = capture == cudaStreamCaptureStatusNone ? attrs : attrs + 1;
+  cfg.numAttrs = capture == cudaStreamCaptureStatusNone ? 1 : 0;
   if (p.direct) {
     cfg.gridDim = dim3(unsigned(segments) * p.direct);
-    cfg.blockDim = dim3(NW * 32);
-    cfg.dynamicSmemBytes = Sh::kSmem;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = p.direct;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = p.direct;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
     return cudaLaunchKernelEx(&cfg, kernel, p, maps);
   }
-  p.grid = sms;
   p.ranges = sms * NT;
   const int64_t blocks = (int64_t(p.max_pages) * p.page_size + KB - 1) / KB + 1 + kSwitchBlocks;
   p.unit_shift = 0;
   while (segments * ((blocks >> p.unit_shift) + 1) >= (int64_t(1) << 31)) ++p.unit_shift;
-  kernel<<<p.grid, NW * 32, Sh::kSmem, s>>>(p, maps);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cfg.gridDim = dim3(sms);
+  if ((e = cudaLaunchKernelEx(&cfg, kernel, p, maps)) != cudaSuccess) return e;
   // 32 warps per query head where a segment has 16 parts and more and two such
   // blocks per SM suffice (152 parts take 2 us so, 10 us with 8 warps; 1024 heads of
   // 19 parts take 13 us less with 8); then 8 warps, and one where the GPU does not
@@ -1460,8 +1473,9 @@ cudaError_t launch_shape(DecodeParams p, Kernel with_tma, Kernel without, int sm
   cfg.gridDim = dim3(unsigned(by_segment ? segments : p.ranges),
                      unsigned(warps > 1 ? p.slot_rows : (p.slot_rows + 7) / 8));
   cfg.blockDim = dim3(warps == 32 ? 1024 : 256);
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.dynamicSmemBytes = 0;
+  cfg.attrs = attrs;
+  cfg.numAttrs = 1;
   return warps == 32  ? cudaLaunchKernelEx(&cfg, join_kernel<T, D, KB, 32>, p, by_segment)
          : warps == 8 ? cudaLaunchKernelEx(&cfg, join_kernel<T, D, KB, 8>, p, by_segment)
                       : cudaLaunchKernelEx(&cfg, join_kernel<T, D, KB, 1>, p, by_segment);

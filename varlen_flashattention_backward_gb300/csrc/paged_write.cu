@@ -35,6 +35,7 @@ __device__ __forceinline__ void store_once<uint4>(uint4 *p, uint4 v) {
 template <typename V, int U>
 __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ WriteParams p,
                                                          int esize) {
+  asm volatile("griddepcontrol.launch_dependents;");   // a decode may be launched behind it
   const int per = int(sizeof(V)) / esize;         // elements per piece
   const unsigned head_v = p.d / per;              // pieces per head
   const unsigned row_v = p.n_kv * head_v;         // ... and per token
