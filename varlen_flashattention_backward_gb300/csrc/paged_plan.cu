@@ -78,6 +78,12 @@ __device__ __forceinline__ int wrap(int64_t i, int n) { return int(i >= n ? i - 
 // over many CTAs, each of which does phase 1 for itself, and leaves phase 3 to
 // one more CTA, launched as their dependent: it does its phase 1 beside them
 // and writes when they are done.
+//
+// Bound by latency: a chain of four dependent accesses (lengths, two prefix sums
+// with a barrier each, the entry of ring or table, the slot) and the launch.  A
+// step of 256 requests takes 6.0 us; 256 requests of which half take prompts of up to
+// 4096 tokens and a fifth end (400000 slots) 9.8 us.  Their bytes would take less than
+// 0.01 and 0.5 us.
 enum : int { kFill = 1, kCommit = 2 };
 
 __global__ void __launch_bounds__(kThreads, 1) plan_kernel(const __grid_constant__ PlanParams p) {
@@ -251,10 +257,15 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(const __grid_constant
 cudaError_t launch_paged_plan(const PlanParams &p0, cudaStream_t s) {
   PlanParams p = p0;
   // Items of work that the host can see: rows, and the pages that requests may
-  // give back.  One CTA does 32768 in about the time of a second launch.
+  // give back.  One CTA where each thread has at most one request and two rows: one
+  // new token each for 64, 256, 512 requests takes it 5.8, 6.0, 6.4 us, many CTAs 6.0,
+  // 6.4, 6.8 and a second launch, but 600 requests take 8.2 and 6.8, and 64 requests of
+  // 16, 64, 500 new tokens 7.3, 9.7, 28 and 7.2, 7.5, 8.0.  The bound on pages is for the
+  // step that ends all requests at once (256 that give back 8192, 32768 pages: 11.5, 27
+  // us and 6.2, 7.4); a usual one gives back few.
   const int64_t items = p.max_tokens + int64_t(p.batch) * p.max_pages;
   p.phases = kFill | kCommit;
-  if (items <= 32768) {
+  if (p.batch <= kThreads && p.max_tokens <= 2 * kThreads && items <= 32768) {
     plan_kernel<<<1, kThreads, 0, s>>>(p);
     return cudaGetLastError();
   }
