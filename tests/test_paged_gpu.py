@@ -2,6 +2,8 @@
 attention, each against its float64 (or whole-number) oracle, and all three
 together as a decoding loop."""
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -252,6 +254,35 @@ def test_decode_large_batches(dtype, batch, heads, heads_kv, shortest, page):
     lens = np.random.default_rng(batch).integers(shortest, 2500, batch)
     lens[3] = 0
     run_decode(dtype, lens, heads, heads_kv, 32, page, seed=batch)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("gap", [10.25, 15.5, 20.75, 26.5])
+@pytest.mark.parametrize("heads", [1, 16])
+def test_decode_many_light_keys(dtype, gap, heads):
+    # Key 0 weighs 1 and holds zeros; 4096 others weigh 2^-gap each and hold 1024, so
+    # y = 4096 1024 2^-gap / (1 + 4096 2^-gap) comes from the light ones alone.  Scores
+    # and values are exact.  Besides y's rounding, half a step: the exponent is off by
+    # at most three roundings (scale log2 e, a product, a difference) of numbers below
+    # 2^5, 3 2^5 2^-24 ln 2 < 2^-17; the weight in two 16-bit parts by 2^-17; exponential,
+    # sums (at most 6 blocks of 16 keys in a team, then 64 parts) and quotient by less
+    # than 128 2^-23 = 2^-16.  In all 2^-15.
+    t, dim, n = DTYPE[dtype], 64, 4097
+    k, v = torch.zeros(2, 258, 16, 1, dim)
+    k.view(-1, dim)[1:n, 5] = -gap
+    v.view(-1, dim)[1:n] = 1024
+    q = torch.zeros(1, heads, dim)
+    q[:, :, 5] = 1
+    qd, kd, vd = (x.to(t).to(DEV) for x in (q, k, v))
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    weight = 4096 * 2.0 ** -gap
+    want = weight * 1024 / (1 + weight)
+    for width in (257, 3000):          # directly, and by ranges
+        table = torch.zeros(1, width, dtype=torch.int32, device=DEV)
+        table[0, :257] = torch.arange(257)
+        y, _, _ = fa.paged_decode(qd, kd, vd, table, lens, math.log(2.0))
+        off = np.abs(f64(y) - want).max() / want
+        assert off <= torch.finfo(t).eps / 2 + 2.0 ** -15
 
 
 def test_decode_all_empty():

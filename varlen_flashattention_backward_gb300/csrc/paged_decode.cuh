@@ -17,7 +17,9 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kFull = 0xffffffffu;
-// Beginning a segment costs a warp about as much as this many blocks of keys.
+// Beginning a segment costs a warp about as much as this many blocks of keys (0, 1, 2
+// and 4 measure alike but where requests are short: 61 of up to 1024 keys 18.2 us
+// with 0, 15.1 with 1).
 constexpr int kSwitchBlocks = 1;
 // Most CTAs of a cluster that shares a segment, and blocks for each team of it (16
 // requests of 512 keys, 8 key heads: 8.7 us so, 13.0 by ranges).
@@ -31,9 +33,10 @@ constexpr int kDirectBlocks = 8;
 // keys are cut into blocks of KB (at least one, which may hold no key).  The
 // segments, each weighing its blocks plus kSwitchBlocks, form a line that is
 // cut into ranges of equal weight, one per team of TW warps of the grid (a team
-// shares its blocks; each of its warps has its own R / TW query heads).  Weights count in
-// units of 2^unit_shift blocks, which the host chooses so that 32 bits hold the
-// line's length; the shift is 0 for any batch that fits a GPU's memory.
+// shares its blocks; each of its warps has its own R / TW query heads).  Weights
+// count in units of 2^unit_shift blocks, which the host chooses so that 32 bits hold
+// the line's length whatever the lengths; the shift is 0 up to a product of
+// segments and longest length, in blocks, of 2^31.
 //
 // A team's share of a segment is a part.  A part that is a whole segment
 // writes y from the warps' registers.  Of the others a team has at most two,
@@ -88,7 +91,7 @@ struct Place {
   int units;         // of each of the request's segments
 };
 
-// The units of requests 32 i + lane.
+// The units of each of request b's segments, 0 behind the last request.
 template <int KB>
 __device__ __forceinline__ int units_at(const DecodeParams &p, int b, bool &bad) {
   if (b >= p.batch) return 0;
@@ -199,10 +202,10 @@ enum : int {
 
 // Shared memory of one kernel of NW warps: a ring of S stages (K and V block
 // each) per team, then per warp QS places for query rows that wait for their
-// part and kExtra bytes more.  The sum of the whole CTA takes the latter's
-// place in the end.  Query rows are fetched ahead where that leaves three
-// stages: under load a fetch takes 1 to 2 us, which a warp would spend waiting at
-// each of its parts.
+// part and EXTRA bytes more.  In the end the sum of the whole CTA takes the place
+// behind the rings.  Query rows are fetched ahead where that leaves three stages:
+// under load a fetch takes 1 to 2 us, which a warp would spend waiting at each of its
+// parts (1024 requests of 64 keys, 32 / 8 heads, D 128: 91 us without, 75 with).
 template <typename T, int D, int RW, int TW, int KB, int EXTRA>
 struct Shape {
   static constexpr int R = RW * TW;
@@ -219,7 +222,8 @@ struct Shape {
   // Most stages, up to 8, that fit.
   static constexpr int fit(int nw, int qs) {
     int s = 8;
-    while (s > 0 && nw / TW * s * kStage + nw * (qs * kQ + EXTRA) + static_bytes(nw, s) > 227 * 1024)
+    while (s > 0 &&
+           nw / TW * s * kStage + nw * (qs * kQ + EXTRA) + static_bytes(nw, s) > 227 * 1024)
       --s;
     return s;
   }
@@ -719,15 +723,29 @@ template <int D, int R>
 using TcShape = Shape<__half, D, TcTeam<R>::RW, TcTeam<R>::TW, 16, 0>;
 
 // S = Q K^T and O = P V by m16n8k16 products: Q's rows are the group's query
-// heads, padded to 16, and a team takes 16 keys at a time through its own ring
-// of stages, filled by cp.async ahead of use.  A K block's place is filled
-// again as soon as S is computed, a V block's after O.
+// heads, padded to 16, and a team takes 16 keys at a time through its own ring of
+// S stages (K and V), S - 1 of which are on the way: the stage read in one step is
+// filled again in the next.  The maximum and the sum run along; O is corrected only
+// in steps in which some row's maximum grows.
 //
 // P goes into the second product as the sum of two 16-bit numbers, so that
-// its rounding (2^-17 for bf16) stays below y's own.  With 8 rows the two
-// halves share one product: rows 0-7 hold P rounded, rows 8-15 what is left
+// its rounding (2^-17 for bf16, 2^-23 for fp16) stays below y's own.  With 8 rows the
+// two halves share one product: rows 0-7 hold P rounded, rows 8-15 what is left
 // of it, and the halves of the result are added at the end.  With 16 rows they
-// are two products.
+// are two products.  fp16 gets P times 2^15, which its range allows, and O is scaled
+// back at a part's end: without that a weight below 2^-14 of the row's largest would
+// lose digits, and one below 2^-25 all of them, which many keys can add up to much of y.
+//
+// Bound by memory for a few query heads per key head: each key is read once, for
+// 4 R operations per element.  One CTA of 8 warps per SM, each with a ring of its
+// own, because what keeps HBM busy is bytes on the way (150 to 200 KB per SM) and no
+// warp has to meet another; mma.sync rather than tcgen05, because 8 or 16 rows
+// would fill an eighth of the latter's 128.  64 requests of 2048 keys, 32 / 8 heads,
+// D 128, bf16: 89 us, 6.0 TB/s, 26% of the issue slots; a warp waits for its copies
+// and for latencies (products, exponentials, shuffles) in equal parts.  From about
+// 16 rows the products' latency bounds it (32 requests of 2000 to 8192 keys, 32 heads
+// on one, D 192: 39 us, 107 TFLOP/s).  Not faster: a warp that only loads, K and V awaited apart, ranges
+// taken from a counter.
 template <typename T, int D, int R, bool kTma>
 __global__ void __launch_bounds__(TcShape<D, R>::NW * 32, 1)
 decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ DecodeMaps maps) {
@@ -736,6 +754,7 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   constexpr int RW = TcTeam<R>::RW, TW = TcTeam<R>::TW;
   constexpr int KB = 16, S = Sh::S, NW = Sh::NW, NT = Sh::NT;
   constexpr int NR = RW / 8;        // rows of a lane
+  constexpr float kUp = std::is_same<T, __half>::value ? 32768.f : 1.f;   // P's factor
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Partials<NT, R> s_part;
   __shared__ uint64_t s_full[NT][S];
@@ -933,9 +952,10 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
       l[i] += (s[i][0] + s[i][1]) + (s[i][2] + s[i][3]);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        hi[i][h] = pack2<T>(s[i][2 * h], s[i][2 * h + 1]);
+        const float p0 = s[i][2 * h] * kUp, p1 = s[i][2 * h + 1] * kUp;
+        hi[i][h] = pack2<T>(p0, p1);
         const float2 back = unpack2<T>(hi[i][h]);
-        lo[i][h] = pack2<T>(s[i][2 * h] - back.x, s[i][2 * h + 1] - back.y);
+        lo[i][h] = pack2<T>(p0 - back.x, p1 - back.y);
       }
     }
 #pragma unroll
@@ -964,6 +984,12 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
       for (int i = 0; i < NR; ++i) {
         l[i] += __shfl_xor_sync(kFull, l[i], 1);
         l[i] += __shfl_xor_sync(kFull, l[i], 2);
+      }
+      if constexpr (kUp != 1.f) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[i][k] *= 1.f / kUp;
       }
       if (opens && ends) {
 #pragma unroll
@@ -1034,8 +1060,14 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
 template <int D, int R>
 using SimtShape = Shape<float, D, R, 1, 8, 8 * R * 4>;
 
-// A warp takes 8 keys at a time.  Scores: four lanes per key, each a quarter
-// of the dims (every fourth chunk).  Output: each lane D / 32 dims of all R heads.
+// Products in full fp32, which no tensor instruction offers.  A warp takes 8 keys at a
+// time.  Scores: four lanes per key, each a quarter of the dims (every fourth chunk),
+// so that a sum needs two shuffles and the banks do not collide.  Output: each lane
+// D / 32 dims of all R heads, in registers; the keys' weights pass through shared
+// memory.  Bound by memory with one or two heads per key head (16 requests of 2048
+// keys, 8 heads each with its own keys, D 128: 48 us, 5.6 TB/s), by the loads of query
+// rows from shared memory, one per key and head, above that (32 heads on 8: 63 us; 64:
+// 96 us).
 template <int D, int R, bool kTma>
 __global__ void __launch_bounds__(SimtShape<D, R>::NW * 32, 1)
 decode_simt_kernel(const __grid_constant__ DecodeParams p,
@@ -1259,6 +1291,10 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
 // done.  Block x takes segment x, or, where there are more segments than ranges,
 // the segment in which range x ends.  WPR warps take a query head's parts in turn,
 // so that their loads overlap, and meet in shared memory, always in the same order.
+// Bound by latency: a chain of two dependent loads (lengths, parts) and the launch,
+// of which the first and the last hide behind the main kernel.  About 3 us of a call
+// that is cut (16 requests of 512 keys: 13.0 us, of which 8.7 remain without the join
+// and the search for ranges).
 // ---------------------------------------------------------------------------
 template <typename T, int D, int KB, int WPR>
 __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256) join_kernel(
@@ -1409,9 +1445,10 @@ bool make_page_maps(DecodeMaps &maps, const DecodeParams &p) {
   };
   if (!nested(false) && !nested(true)) return false;
   const cuuint32_t ones[4] = {1, 1, 1, 1};
-  const CUtensorMapDataType type = std::is_same<T, float>::value    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                   : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapDataType type =
+      std::is_same<T, float>::value    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+      : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const auto encode = [&](CUtensorMap *map, const void *base) {
     return enc(map, type, 4, const_cast<void *>(base), dims, strides, box, ones,
                CU_TENSOR_MAP_INTERLEAVE_NONE,
