@@ -1064,9 +1064,11 @@ using SimtShape = Shape<float, D, R, 1, 8, 8 * R * 4>;
 // time.  Scores: four lanes per key, each a quarter of the dims (every fourth chunk),
 // so that a sum needs two shuffles and the banks do not collide.  Output: each lane
 // D / 32 dims of all R heads, in registers; the keys' weights pass through shared
-// memory.  Bound by memory with one or two heads per key head (16 requests of 2048
-// keys, 8 heads each with its own keys, D 128: 48 us, 5.6 TB/s), by the loads of query
-// rows from shared memory, one per key and head, above that (32 heads on 8: 63 us; 64:
+// memory.  Query rows are read from registers where a lane's quarter of them takes at
+// most 128 (R D <= 512), else from shared memory for every block of keys.  Bound by
+// memory with one or two heads per key head (16 requests of 2048 keys, 8 heads each
+// with its own keys, D 128: 47 us, 5.7 TB/s), by shared memory and shuffles above that
+// (32 heads on 8: 52 us, 62 with the rows in shared memory; 64 on 8, where they are:
 // 96 us).
 template <int D, int R, bool kTma>
 __global__ void __launch_bounds__(SimtShape<D, R>::NW * 32, 1)
@@ -1078,6 +1080,7 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
   constexpr int CPR = D / 4;
   constexpr int VW = D % 128 == 0 ? 4 : D % 64 == 0 ? 2 : 1;   // dims per access
   constexpr int NV = D / (32 * VW);                             // accesses per row
+  constexpr bool kQRegs = R * D <= 512;   // query rows in registers
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Partials<NW, R> s_part;
   __shared__ uint64_t s_full[NW][S];
@@ -1117,6 +1120,7 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
   int stage = 0, fill = S - 1, heads = 0, n0 = 0, id = 0, b = 0;
   uint32_t parity = 0;
   float o[R][NV * VW], m[R], l[R];
+  float4 q_own[kQRegs ? R : 1][kQRegs ? CPR / 4 : 1];
   bool opens = false;
 
 #pragma unroll 1
@@ -1153,6 +1157,15 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
         if (kTma) sm103::fence_proxy_async_smem();   // before a later copy to this place
         __syncwarp();
       }
+      if constexpr (kQRegs) {
+#pragma unroll
+        for (int i = 0; i < CPR / 4; ++i) {
+          const int c = (i * 4 + quarter) ^ ((key & 1) << 2);
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            q_own[r][i] = *reinterpret_cast<const float4 *>(s_q + r * D + c * 4);
+        }
+      }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         m[r] = -CUDART_INF_F;
@@ -1172,7 +1185,11 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
       const float4 kv = *reinterpret_cast<const float4 *>(kb + Tl::at(key, c));
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const float4 qv = *reinterpret_cast<const float4 *>(s_q + r * D + c * 4);
+        float4 qv;
+        if constexpr (kQRegs)
+          qv = q_own[r][i];
+        else
+          qv = *reinterpret_cast<const float4 *>(s_q + r * D + c * 4);
         s[r] = fmaf(kv.x, qv.x, s[r]);
         s[r] = fmaf(kv.y, qv.y, s[r]);
         s[r] = fmaf(kv.z, qv.z, s[r]);
