@@ -206,7 +206,7 @@ enum : int {
 // behind the rings.  Query rows are fetched ahead where that leaves three stages:
 // under load a fetch takes 1 to 2 us, which a warp would spend waiting at each of its
 // parts (1024 requests of 64 keys, 32 / 8 heads, D 128: 91 us without, 75 with).
-template <typename T, int D, int RW, int TW, int KB, int EXTRA>
+template <typename T, int D, int RW, int TW, int KB, int EXTRA, int WARPS>
 struct Shape {
   static constexpr int R = RW * TW;
   static constexpr int PAD = 4;
@@ -227,7 +227,7 @@ struct Shape {
       --s;
     return s;
   }
-  static constexpr int NW = fit(8, EXTRA > 0) >= 2 ? 8 : 4;
+  static constexpr int NW = fit(WARPS, EXTRA > 0) >= 2 ? WARPS : 4;
   static constexpr int NT = NW / TW;
   static constexpr int QS = fit(NW, 2) >= 3 ? 2 : (fit(NW, 1) >= 3 || EXTRA > 0) ? 1 : 0;
   static constexpr int S = fit(NW, QS);
@@ -577,7 +577,7 @@ __device__ __forceinline__ void merge_cta(const DecodeParams &p, int chunks,
     const float m = s.m[mine][r], l = s.l[mine][r];
     float mx = m;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    for (int o = 1; o < NT; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
     const float f = sm103::ex2(m - (mx == -CUDART_INF_F ? 0.f : mx));
     float sum = 0.f, acc[D / 32];
 #pragma unroll
@@ -719,8 +719,16 @@ template <int R>
 struct TcTeam {
   static constexpr int RW = R == 8 ? 8 : 16, TW = R / RW;
 };
+// Warps of a CTA.  8 have registers for D up to 192.  With D 32 a block takes a warp
+// little more than latencies, which 16 hide better (16 and 8, in us: 64 requests of 4000
+// keys, 32 heads on 4, 39 and 47; 16 on one 15 and 20; 64 on one 39 and 48; one of 2048
+// keys 7.4 and 7.1), but for 32 rows (32 on one: 32 and 29).  With D 64 they cost what
+// they gain (32 on 4: 67 and 58).
+constexpr int tc_warps(int d, int r) {
+  return d == 32 && r != 32 ? 16 : 8;
+}
 template <int D, int R>
-using TcShape = Shape<__half, D, TcTeam<R>::RW, TcTeam<R>::TW, 16, 0>;
+using TcShape = Shape<__half, D, TcTeam<R>::RW, TcTeam<R>::TW, 16, 0, tc_warps(D, R)>;
 
 // S = Q K^T and O = P V by m16n8k16 products: Q's rows are the group's query
 // heads, padded to 16, and a team takes 16 keys at a time through its own ring of
@@ -737,7 +745,7 @@ using TcShape = Shape<__half, D, TcTeam<R>::RW, TcTeam<R>::TW, 16, 0>;
 // lose digits, and one below 2^-25 all of them, which many keys can add up to much of y.
 //
 // Bound by memory for a few query heads per key head: each key is read once, for
-// 4 R operations per element.  One CTA of 8 warps per SM, each with a ring of its
+// 4 R operations per element.  One CTA of 8 or 16 warps per SM, each with a ring of its
 // own, because what keeps HBM busy is bytes on the way (150 to 200 KB per SM) and no
 // warp has to meet another; mma.sync rather than tcgen05, because 8 or 16 rows
 // would fill an eighth of the latter's 128.  64 requests of 2048 keys, 32 / 8 heads,
@@ -1058,7 +1066,7 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
 // fp32 kernel, on the CUDA cores
 // ---------------------------------------------------------------------------
 template <int D, int R>
-using SimtShape = Shape<float, D, R, 1, 8, 8 * R * 4>;
+using SimtShape = Shape<float, D, R, 1, 8, 8 * R * 4, 8>;
 
 // Products in full fp32, which no tensor instruction offers.  A warp takes 8 keys at a
 // time.  Scores: four lanes per key, each a quarter of the dims (every fourth chunk),
