@@ -7,6 +7,7 @@ import math
 import numpy as np
 import pytest
 import torch
+import torch.nn.functional as F
 
 import oracle
 from oracle import paged as po
@@ -549,6 +550,86 @@ def test_prompt_then_steps_equal_the_packed_forward(dtype):
     taken = table[3, -(-total[3] // page):].tolist()
     assert int(err) == 0 and set(held) <= set(taken) | set(
         ring[(int(state[0]) + torch.arange(int(state[1]))) % n_pages].tolist())
+
+
+def test_large_plan_in_a_graph():
+    """A plan of many rows, updated in place and captured: every replay goes on
+    from where the one before ended."""
+    rng = np.random.default_rng(4)
+    b, page, width, n_pages, max_tokens = 40, 16, 64, 3000, 6000
+    table, lens, delta, ring, state = random_plan(rng, b, page, width, 120, n_pages)
+    t = [dev(table, torch.int32), dev(lens, torch.int32), dev(delta, torch.int32),
+         dev(ring, torch.int32), dev(state, torch.int64)]
+    first = [x.clone() for x in t]
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def step():
+        return fa.paged_plan(*t, page, max_tokens, seq_lens_out=t[1], free_state_out=t[4], error=err)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    for x, y in zip(t, first):
+        x.copy_(y)
+    err.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        slots, cu, _, _ = step()
+    seen = 0
+    for _ in range(4):
+        graph.replay()
+        ref = oracle.paged_plan(table, lens, delta, ring, state, page, max_tokens)
+        seen |= ref["error"]
+        table, lens, ring, state = (ref[n] for n in ("block_table", "seq_lens", "free_pages",
+                                                     "free_state"))
+        assert np.array_equal(slots.cpu().numpy(), ref["slots"])
+        assert np.array_equal(cu.cpu().numpy(), ref["cu"])
+        for x, want in zip((t[0], t[1], t[3], t[4]), (table, lens, ring, state)):
+            assert np.array_equal(x.cpu().numpy(), want)
+        assert int(err) == seen
+
+
+def test_decode_with_the_widest_table():
+    """A table of 2^30 keys per request, where the line of blocks is measured in
+    units of several."""
+    rng = np.random.default_rng(9)
+    page, width, dim = 65536, 16384, 32
+    lens = np.array([70000, 5, 0, 131072, 1000, 65536, 1] + [300] * 57)
+    pages = sum(-(-int(n) // page) for n in lens)
+    cache = [torch.from_numpy(rng.standard_normal((pages * page, 2, dim), np.float32)).to(torch.bfloat16)
+             .view(pages, page, 2, dim) for _ in range(2)]
+    table, _ = make_table(rng, lens, page, pages, width)
+    q = torch.from_numpy(rng.standard_normal((len(lens), 4, dim)).astype(np.float32)).to(torch.bfloat16)
+    ref = oracle.paged_decode(f64(q), f64(cache[0]), f64(cache[1]), table, lens, 0.2)
+    kd, vd = (x.to(DEV) for x in cache)
+    y, top, total = fa.paged_decode(q.to(DEV), kd, vd, dev(table), dev(lens, torch.int32), 0.2,
+                                    stats=True)
+    check_decode(ref, float(cache[1].float().abs().max()), dim, "bf16", y, top, total)
+
+
+def test_two_graphs_replayed_at_once():
+    runs = []
+    for seed, lens in ((0, [2000, 1500]), (1, [900, 3000, 12])):
+        args, ref, cache = decode_inputs(seed, lens)
+        args = (*args[:3], F.pad(args[3], (0, 3000), value=-1), *args[4:])   # cut and joined
+        stream = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        fa.paged_decode(*args, stream=stream)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            y = fa.paged_decode(*args)[0]
+        runs.append((graph, stream, y, ref, float(cache[1].float().abs().max()), args))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, stream, *_ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, y, ref, v_max, _ in runs:
+        check_decode(ref, v_max, 64, "bf16", y)
 
 
 def test_statistics_feed_the_backward():
