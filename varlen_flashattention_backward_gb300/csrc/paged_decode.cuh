@@ -723,9 +723,12 @@ struct TcTeam {
 // little more than latencies, which 16 hide better (16 and 8, in us: 64 requests of 4000
 // keys, 32 heads on 4, 39 and 47; 16 on one 15 and 20; 64 on one 39 and 48; one of 2048
 // keys 7.4 and 7.1), but for 32 rows (32 on one: 32 and 29).  With D 64 they cost what
-// they gain (32 on 4: 67 and 58).
+// they gain (32 on 4: 67 and 58).  With D 192 and 16 rows 8 warps have room for two
+// stages each, of which one is on the way; 4 have four (4 and 8, in us: 32 requests of
+// 5000 keys, 16 heads on one, 32 and 37; 500 of up to 200, 32 on two, 38 and 46; one of
+// 2048 12.4 and 13.6; but 16 of 2048, 32 on two, 20.3 and 16.4).
 constexpr int tc_warps(int d, int r) {
-  return d == 32 && r != 32 ? 16 : 8;
+  return d == 32 && r != 32 ? 16 : d == 192 && r == 16 ? 4 : 8;
 }
 template <int D, int R>
 using TcShape = Shape<__half, D, TcTeam<R>::RW, TcTeam<R>::TW, 16, 0, tc_warps(D, R)>;
@@ -745,7 +748,7 @@ using TcShape = Shape<__half, D, TcTeam<R>::RW, TcTeam<R>::TW, 16, 0, tc_warps(D
 // lose digits, and one below 2^-25 all of them, which many keys can add up to much of y.
 //
 // Bound by memory for a few query heads per key head: each key is read once, for
-// 4 R operations per element.  One CTA of 8 or 16 warps per SM, each with a ring of its
+// 4 R operations per element.  One CTA of 4 to 16 warps per SM, each with a ring of its
 // own, because what keeps HBM busy is bytes on the way (150 to 200 KB per SM) and no
 // warp has to meet another; mma.sync rather than tcgen05, because 8 or 16 rows
 // would fill an eighth of the latter's 128.  64 requests of 2048 keys, 32 / 8 heads,
