@@ -526,8 +526,10 @@ fa_status fa_paged_decode_workspace_size(int64_t batch, int64_t head_num, int64_
  *                 written, as fa_varlen_fwd writes them; or both NULL
  * A request with no key to see (length 0, or pre_tokens < 0), or whose every
  * score is -inf, gets y = 0, max = -inf, sum = 0.  What the cache holds behind
- * a request's length, infinities and NaN too, has no influence.  The result
- * does not change from run to run on one device (fixed add order).
+ * a request's length, infinities and NaN too, has no influence.  (An infinite
+ * value among the keys that count makes its column infinite in fp32, and infinite
+ * or NaN in fp16 and bf16, whose weights are multiplied in two parts.)  The result does not
+ * change from run to run on one device (fixed add order).
  * workspace: 16-byte aligned (FA_ERR_INVALID otherwise), at least what
  * fa_paged_decode_workspace_size gives; NULL where that is 0. */
 fa_status fa_paged_decode(const fa_paged_decode_args *args, fa_stream_t stream);

@@ -322,6 +322,21 @@ def test_decode_scores_of_minus_infinity(dtype):
     assert (y[1] == 0).all() and (top[1] == -np.inf).all() and (total[1] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_decode_infinite_values_stay_in_their_column(dtype):
+    # One value of one key head is infinite: its column of that head's queries is
+    # infinite (fp32) or NaN, everything else as without it.
+    (q, k, v, table, lens, scale), ref, cache = decode_inputs(4, [40, 300], dtype=dtype)
+    v[table[1, 2].long(), 5, 1, 7] = float("inf")
+    y, top, total = fa.paged_decode(q, k, v, table, lens, scale, stats=True)
+    hit = torch.zeros_like(y, dtype=torch.bool)
+    hit[1, 4:, 7] = True
+    bad = y[hit]
+    assert (bad == float("inf")).all() if dtype == "fp32" else not torch.isfinite(bad).any()
+    y[hit] = torch.from_numpy(ref["y"]).to(y)[hit]
+    check_decode(ref, float(cache[1].float().abs().max()), 64, dtype, y, top, total)
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("page", [4, 16, 48])
 def test_decode_bad_pages_and_lengths(dtype, page):
