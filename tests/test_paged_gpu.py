@@ -248,6 +248,14 @@ def test_decode_batches(batch, length):
     run_decode("bf16", lens, 2, 1, 32, 16, seed=batch)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("batch", [152, 153, 304, 305])
+def test_decode_one_or_two_waves(dtype, batch):
+    # One CTA per request up to twice the GPU's SMs, ranges above.
+    lens = np.random.default_rng(batch).integers(0, 200, batch)
+    run_decode(dtype, lens, 3, 1, 64, 16, seed=batch)
+
+
 @pytest.mark.parametrize("dtype,batch,heads,heads_kv,shortest,page", [
     ("bf16", 40, 16, 8, 1500, 16), ("fp16", 100, 64, 2, 1600, 24), ("fp32", 20, 8, 8, 1500, 32)])
 def test_decode_large_batches(dtype, batch, heads, heads_kv, shortest, page):
