@@ -91,11 +91,28 @@ struct Place {
   int units;         // of each of the request's segments
 };
 
+// The length that request b holds.  A kernel of this file may be on the GPU while
+// the one before it still writes lengths, tables and rows, so none of them is read
+// through the read-only path, which asks for memory that nobody writes as long as the
+// reader lives: the main kernel reads them by plain loads behind its wait, and the
+// join, which looks at lengths ahead of its own wait (the main kernel, behind its, let
+// it start), at the L2, where that kernel's wait has seen them arrive.
+template <bool kAhead = false>
+__device__ __forceinline__ int length_of(const DecodeParams &p, int b) {
+  if constexpr (kAhead) {
+    int len;
+    asm("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(len) : "l"(p.lens + b));   // any time will do
+    return len;
+  } else {
+    return p.lens[b];
+  }
+}
+
 // The units of each of request b's segments, 0 behind the last request.
-template <int KB>
+template <int KB, bool kAhead>
 __device__ __forceinline__ int units_at(const DecodeParams &p, int b, bool &bad) {
   if (b >= p.batch) return 0;
-  const int len = __ldg(p.lens + b);
+  const int len = length_of<kAhead>(p, b);
   bad |= len < 0 || len > p.max_pages * p.page_size;
   return units_of(p, span_of<KB>(p, len).blocks);
 }
@@ -106,7 +123,7 @@ __device__ __forceinline__ int units_at(const DecodeParams &p, int b, bool &bad)
 // those 1024 further on), then the warp looks at the 32 that hold the unit.
 // False: nothing is there.  (The indexes are held in bounds for the sake of
 // lengths that change during the call, which is an error of the caller's.)
-template <int KB>
+template <int KB, bool kAhead>
 __device__ __forceinline__ bool find(const DecodeParams &p, int segs, int range, int before,
                                      Line &line, Place &at) {
   const int lane = threadIdx.x & 31;
@@ -116,7 +133,7 @@ __device__ __forceinline__ bool find(const DecodeParams &p, int segs, int range,
   bool bad = false;
 #pragma unroll 8
   for (int i = 0; i < rows; ++i) {
-    units = units_at<KB>(p, i * 32 + lane, bad);
+    units = units_at<KB, kAhead>(p, i * 32 + lane, bad);
     const int all = __reduce_add_sync(kFull, units);
     if (lane == (i & 31)) sum[i >> 5] = all;
   }
@@ -141,7 +158,7 @@ __device__ __forceinline__ bool find(const DecodeParams &p, int segs, int range,
                   __popc(__ballot_sync(kFull, upto[1] * segs <= u));
   int from = row < 32 ? __shfl_sync(kFull, upto[0] - sum[0], row)
                       : __shfl_sync(kFull, upto[1] - sum[1], row - 32);
-  if (rows > 1) units = units_at<KB>(p, row * 32 + lane, bad);
+  if (rows > 1) units = units_at<KB, kAhead>(p, row * 32 + lane, bad);
   int x = units;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -158,21 +175,21 @@ __device__ __forceinline__ bool find(const DecodeParams &p, int segs, int range,
 }
 
 // Measures the line and gives the first unit of segment (at.b, at.seg), whose
-// units it fills in.
+// units it fills in.  For the join.
 template <int KB>
 __device__ __forceinline__ int segment_start(const DecodeParams &p, int segs, Place &at,
                                              Line &line) {
   int sum = 0, before = 0;
   bool bad = false;
   for (int b = threadIdx.x & 31; b < p.batch; b += 32) {
-    const int units = units_at<KB>(p, b, bad);
+    const int units = units_at<KB, true>(p, b, bad);
     sum += units;
     if (b < at.b) before += units;
   }
   const int total = __reduce_add_sync(kFull, sum) * segs;
   line.each = total / p.ranges;
   line.rest = total - line.each * p.ranges;
-  at.units = units_of(p, span_of<KB>(p, __ldg(p.lens + at.b)).blocks);
+  at.units = units_of(p, span_of<KB>(p, length_of<true>(p, at.b)).blocks);
   at.off = 0;
   return __reduce_add_sync(kFull, before) * segs + at.seg * at.units;
 }
@@ -318,7 +335,7 @@ struct Loader {
       const int cta = blockIdx.x / p.direct, teams = p.direct * Sh::NT;
       b = cta / segs;
       seg = cta - b * segs;
-      const int len = __ldg(p.lens + b);
+      const int len = length_of(p, b);
       if ((len < 0 || len > p.max_pages * p.page_size) && p.error)
         atomicOr(p.error, FA_PAGED_BAD_LENGTH);
       // Its share as a range whose units are blocks.
@@ -333,7 +350,7 @@ struct Loader {
     const int range = blockIdx.x * Sh::NT + team;
     Line line;
     Place at;
-    if (find<KB>(p, segs, range, 0, line, at)) {
+    if (find<KB, false>(p, segs, range, 0, line, at)) {
       left = line.each + (range < line.rest ? 1 : 0);
       b = at.b;
       seg = at.seg;
@@ -344,7 +361,7 @@ struct Loader {
 
   // Request b's span (its segments have the same).
   __device__ __forceinline__ void enter() {
-    span = span_of<KB>(p, __ldg(p.lens + b));
+    span = span_of<KB>(p, length_of(p, b));
     units = units_of(p, span.blocks);
   }
 
@@ -355,7 +372,7 @@ struct Loader {
   __device__ __forceinline__ void load_pages() {
     page_lane = 0;
     const int j = row + lane * KB;
-    if (j < span.hi) page = __ldg(p.table + block_b * p.table_stride + page_index(j));
+    if (j < span.hi) page = p.table[block_b * p.table_stride + page_index(j)];
   }
 
   // The next part: the rest of the range inside the current segment.
@@ -418,7 +435,7 @@ struct Loader {
       if ((what >> (lane % KB)) & 1) {
         const int j = row + lane % KB, idx = page_index(j);
         tok = j - idx * p.page_size;
-        page = __ldg(p.table + block_b * p.table_stride + idx);
+        page = p.table[block_b * p.table_stride + idx];
       }
     }
   }
@@ -617,7 +634,7 @@ __device__ __forceinline__ void join_cluster(const DecodeParams &p, int chunks,
   const int lane = threadIdx.x & 31, segs = p.n_kv * chunks;
   const int id = blockIdx.x / p.direct;
   const int b = id / segs, seg = id - b * segs;
-  const int blocks = span_of<KB>(p, __ldg(p.lens + b)).blocks;
+  const int blocks = span_of<KB>(p, length_of(p, b)).blocks;
   const int per = (blocks + p.direct * NT - 1) / (p.direct * NT);
   const int parts = (blocks + per * NT - 1) / (per * NT);   // CTAs that have blocks
   int r = (blockIdx.x - id * p.direct) * NW + (threadIdx.x >> 5);
@@ -1164,7 +1181,7 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
       s_q = reinterpret_cast<float *>(extra + load.parts_free % Sh::QS * Sh::kQ);
       if (!(what & kRowsFetched)) {
         const float *qr = static_cast<const float *>(p.q) + b * p.q_stride + int64_t(n0) * D;
-        for (int i = lane; i < heads * D; i += 32) s_q[i] = __ldg(qr + i);
+        for (int i = lane; i < heads * D; i += 32) s_q[i] = qr[i];
         if (kTma) sm103::fence_proxy_async_smem();   // before a later copy to this place
         __syncwarp();
       }
@@ -1332,23 +1349,42 @@ __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256) join_kernel(
   constexpr int U = WPR > 8 ? 4 : 2;   // parts on the way at once, per warp
   __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
   __shared__ float s_o[WPR > 1 ? kJoinWarps : 1][D];
+  __shared__ int s_b, s_seg, s_first, s_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunks = (p.group + p.rows - 1) / p.rows, segs = p.n_kv * chunks;
-  Line line;
-  Place at{0, 0, 0, 1};
-  int first_unit;                    // of the segment
-  if (by_segment) {
-    at.b = blockIdx.x / segs;
-    at.seg = blockIdx.x - at.b * segs;
-    first_unit = segment_start<KB>(p, segs, at, line);
-  } else {
-    find<KB>(p, segs, blockIdx.x + 1, 1, line, at);
-    first_unit = line.start(blockIdx.x + 1) - 1 - at.off;
+  // The lengths come past the L1 (length_of), so one warp reads them for all (eight:
+  // 1024 requests of 64 keys 80 us, one: 69), but where they are few and the blocks many
+  // each for itself (64 of 2048 keys, 32 heads on 8: 91.5 us, with one 94).
+  int b = 0, seg = 0, i = 0, last = 0;
+  const bool alone = WPR == 1 && by_segment;
+  if (alone || warp == 0) {
+    Line line;
+    Place at{0, 0, 0, 1};
+    int first_unit;                  // of the segment
+    if (by_segment) {
+      at.b = blockIdx.x / segs;
+      at.seg = blockIdx.x - at.b * segs;
+      first_unit = segment_start<KB>(p, segs, at, line);
+    } else {
+      find<KB, true>(p, segs, blockIdx.x + 1, 1, line, at);
+      first_unit = line.start(blockIdx.x + 1) - 1 - at.off;
+    }
+    b = at.b;
+    seg = at.seg;
+    i = line.range_of(first_unit + (kSwitchBlocks >> p.unit_shift));
+    last = min(line.range_of(first_unit + at.units - 1), p.ranges - 1);
+    if (!alone && lane == 0) {
+      s_b = b;
+      s_seg = seg;
+      s_first = i;
+      s_last = last;
+    }
   }
-  // The ranges of its first and last block.
-  const int i = line.range_of(first_unit + (kSwitchBlocks >> p.unit_shift));
-  const int last = min(line.range_of(first_unit + at.units - 1), p.ranges - 1);
-  const int hk = chunks == 1 ? at.seg : at.seg / chunks, h0 = (at.seg - hk * chunks) * p.rows;
+  if (!alone) {
+    __syncthreads();
+    b = s_b, seg = s_seg, i = s_first, last = s_last;
+  }
+  const int hk = chunks == 1 ? seg : seg / chunks, h0 = (seg - hk * chunks) * p.rows;
   const int rows = min(p.rows, p.group - h0);
 
   asm volatile("griddepcontrol.launch_dependents;");
@@ -1388,12 +1424,12 @@ __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256) join_kernel(
       }
     }
     const int n = hk * p.group + h0 + r;
-    T *y = static_cast<T *>(p.y) + at.b * p.y_stride + int64_t(n) * D;
+    T *y = static_cast<T *>(p.y) + b * p.y_stride + int64_t(n) * D;
     if constexpr (WPR == 1) {
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
       for (int k = 0; k < PL; ++k) y[lane + 32 * k] = from_f<T>(acc[k] * inv);
-      if (lane == 0) write_stats(p, at.b, n, mx * kLn2, sum);
+      if (lane == 0) write_stats(p, b, n, mx * kLn2, sum);
     } else {
       // All warps are here: WPR is the whole block, and r its row.
       __syncthreads();
@@ -1418,7 +1454,7 @@ __global__ void __launch_bounds__(WPR > 8 ? WPR * 32 : 256) join_kernel(
           out += f * s_o[k][d];
         }
         y[d] = from_f<T>(total == 0.f ? 0.f : out / total);
-        if (d == 0) write_stats(p, at.b, n, top * kLn2, total);
+        if (d == 0) write_stats(p, b, n, top * kLn2, total);
       }
     }
   }
