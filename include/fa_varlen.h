@@ -398,7 +398,8 @@ fa_status fa_varlen_bwd_schedule_ex(const int64_t *seq_lens_q, const int64_t *se
  *                        given back than it has room for; the call changes
  *                        nothing
  *   FA_PAGED_TIMEOUT     decode: a bounded in-kernel wait expired; the results
- *                        are invalid
+ *                        are invalid (nothing else tells: with error NULL they
+ *                        come back as if they were good)
  *   FA_PAGED_BAD_SLOT    write: a slot at or above num_pages * page_size,
  *                        whose row is skipped
  * Limits (FA_ERR_INVALID): batch in [1, 2048]; num_pages in [1, 2^31);
@@ -533,6 +534,13 @@ fa_status fa_paged_decode_workspace_size(int64_t batch, int64_t head_num, int64_
  * workspace: 16-byte aligned (FA_ERR_INVALID otherwise), at least what
  * fa_paged_decode_workspace_size gives; NULL where that is 0. */
 fa_status fa_paged_decode(const fa_paged_decode_args *args, fa_stream_t stream);
+
+/* fa_paged_decode with options; NULL gives the defaults. */
+typedef struct {
+  int64_t wait_timeout_ns; /* bound on every in-kernel wait; <= 0: 2 s */
+} fa_paged_decode_options;
+fa_status fa_paged_decode_ex(const fa_paged_decode_args *args,
+                             const fa_paged_decode_options *options, fa_stream_t stream);
 
 /* Library version: major * 10000 + minor * 100 + patch. */
 int32_t fa_varlen_version(void);

@@ -93,6 +93,7 @@ _SIGS = {
     "fa_paged_write": ([_cp, _vp], _i32),
     "fa_paged_decode_workspace_size": ([_i64] * 4 + [_i32] + [_i64] * 3 + [_psz], _i32),
     "fa_paged_decode": ([_cp, _vp], _i32),
+    "fa_paged_decode_ex": ([_cp, _cp, _vp], _i32),
 }
 
 EXPORTS = tuple(_SIGS)
@@ -409,6 +410,7 @@ def _format(names):
 
 _pack_plan, _pack_write, _pack_decode = (_format(n).pack
                                          for n in (PLAN_ARGS, WRITE_ARGS, DECODE_ARGS))
+_pack_options = _format(["wait_timeout_ns"]).pack
 
 
 class _On:
@@ -591,16 +593,19 @@ def _decode_workspace(index, *call):
 
 def paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, pre_tokens=2 ** 31 - 1,
                  y=None, stats=False, softmax_max=None, softmax_sum=None, workspace=None,
-                 error=None, stream=None):
+                 error=None, stream=None, wait_timeout_ns=0):
     """(y, softmax_max, softmax_sum) of one query row per request over its
     cached keys (fa_paged_decode).  The statistics ([batch, heads, 8], as
     ``fwd`` gives them) are computed with ``stats`` or when their tensors
-    are given, and None otherwise."""
+    are given, and None otherwise.  ``wait_timeout_ns`` bounds every in-kernel
+    wait (<= 0: 2 s); one that expires adds FA_PAGED_TIMEOUT to ``error``, and
+    without ``error`` nothing tells that the results are invalid."""
     index = _device_of(k_pages, "k_pages and v_pages")
     if _elsewhere(index, stream):
         with _On(index, stream):
             return paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, pre_tokens, y,
-                                stats, softmax_max, softmax_sum, workspace, error)
+                                stats, softmax_max, softmax_sum, workspace, error,
+                                wait_timeout_ns=wait_timeout_ns)
     shape, strides = _pages(k_pages, v_pages, index)
     max_pages, table_stride = _table(block_table, index)
     b, heads, (_, _, n_kv, d) = block_table.size(0), q.shape, shape
@@ -635,13 +640,17 @@ def paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, pre_tokens=2
         if not (workspace.is_contiguous() and workspace.get_device() == index):
             _refuse("workspace", workspace, "contiguous memory", index)
         at_workspace = workspace.data_ptr()
-    status = (_LIB or lib()).fa_paged_decode(_pack_decode(
+    args = _pack_decode(
         q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), shape[0], shape[1], strides[0],
         strides[1], strides[2], block_table.data_ptr(), max_pages, table_stride,
         _flat(seq_lens, torch.int32, b, index, "seq_lens"), b, n, n_kv, d, _DTYPE[dtype], 0, scale,
         min(max(int(pre_tokens), -1), 2 ** 40), y.data_ptr(), ys, top, total,
-        0 if error is None else _flat(error, torch.int32, 1, index, "error"), at_workspace,
-        nbytes), _raw_stream(index))
+        0 if error is None else _flat(error, torch.int32, 1, index, "error"), at_workspace, nbytes)
+    if wait_timeout_ns:
+        status = lib().fa_paged_decode_ex(args, _pack_options(int(wait_timeout_ns)),
+                                          _raw_stream(index))
+    else:
+        status = (_LIB or lib()).fa_paged_decode(args, _raw_stream(index))
     if status:
         _check(status, "fa_paged_decode")
     return y, softmax_max, softmax_sum

@@ -13,6 +13,7 @@ constexpr size_t kAlign = 256;
 constexpr int64_t kMaxPageSize = 65536;
 constexpr int64_t kMaxKeys = int64_t(1) << 30;
 constexpr int64_t kMaxI32 = 2147483647;
+constexpr int64_t kDefaultWaitNs = 2000000000;
 // Extent of one axis (count * stride) in elements: offsets stay inside 64 bits.
 constexpr int64_t kMaxExtent = int64_t(1) << 58;
 
@@ -218,6 +219,11 @@ fa_status fa_paged_decode_workspace_size(int64_t batch, int64_t head_num, int64_
 }
 
 fa_status fa_paged_decode(const fa_paged_decode_args *args, fa_stream_t stream) {
+  return fa_paged_decode_ex(args, nullptr, stream);
+}
+
+fa_status fa_paged_decode_ex(const fa_paged_decode_args *args,
+                             const fa_paged_decode_options *options, fa_stream_t stream) {
   if (!args) return FA_ERR_NULLPTR;
   const auto &a = *args;
   if (a.reserved != 0) return FA_ERR_INVALID;
@@ -290,6 +296,7 @@ fa_status fa_paged_decode(const fa_paged_decode_args *args, fa_stream_t stream) 
   p.pre = int(a.pre_tokens < -1 ? -1 : a.pre_tokens > kMaxKeys ? kMaxKeys : a.pre_tokens);
   p.scale = float(a.scale);
   p.scale_log2 = float(a.scale * 1.4426950408889634);
+  p.wait_ns = options && options->wait_timeout_ns > 0 ? options->wait_timeout_ns : kDefaultWaitNs;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == FA_DTYPE_FP32   ? launch_paged_decode_fp32(p, sms, cs)
                         : dtype == FA_DTYPE_FP16 ? launch_paged_decode_fp16(p, sms, cs)

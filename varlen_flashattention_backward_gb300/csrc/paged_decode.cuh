@@ -290,7 +290,6 @@ __device__ __forceinline__ void tma_load_panels_w(uint32_t dst_k, uint32_t dst_v
       "l"(reinterpret_cast<uint64_t>(&maps.v)), "r"(bar), "r"(x), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
 }
-constexpr long long kWaitNs = 2000000000LL;
 
 // The loading side of a team: walks its range and keeps the ring filled.
 // `look` finds the next block, `issue`, one block later, starts its copies.  All
@@ -519,19 +518,57 @@ __device__ __forceinline__ void clear_rows(uint8_t *v, uint32_t mask) {
   }
 }
 
-// Waits for a stage's copies, at most kWaitNs.  A wait that runs out sets
-// `abort`, after which no wait of the CTA takes long: the call then ends with
-// wrong results and FA_PAGED_TIMEOUT.
-__device__ __forceinline__ void wait_stage(uint32_t bar, uint32_t parity, int *abort) {
-  if (!sm103::mbar_wait(bar, parity, kWaitNs, abort)) *abort = 1;
+// Waits for the phase with parity `parity` to complete, at most `limit` ns, or until
+// *abort (if given) is set by another warp of the CTA whose wait ran out.  A try_wait
+// may sleep for as long as the hardware likes, so short limits are kept by polling.
+__device__ __forceinline__ bool test_phase(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, long long limit,
+                                           const volatile int *abort) {
+  if (test_phase(bar, parity)) return true;
+  const bool sleeps = limit >= 10000000;
+  const uint64_t t0 = sm103::global_timer_ns();
+  while (true) {
+    if (sleeps ? sm103::mbar_try_wait(bar, parity) : test_phase(bar, parity)) return true;
+    if (abort && *abort) return false;
+    if (static_cast<long long>(sm103::global_timer_ns() - t0) > limit) return false;
+  }
 }
 
-// After a wait that ran out: waits, again for a limited time, for the copies that
-// may still be on the way to a ring whose next stage and parity these are.
-__device__ __noinline__ void drain(uint32_t full, int stages, int stage, uint32_t parity) {
-  const int never = 0;
-  for (int i = 0; i < stages; ++i)
-    sm103::mbar_wait(full + i * 8, i < stage ? parity : parity ^ 1, kWaitNs, &never);
+// How a team gives up.  A warp whose wait for a stage runs out (p.wait_ns) goes on to the
+// next step, where it leaves the loop before it refills that stage, whose copies may
+// still be on the way.  The other warps of its team leave there too: in between all meet
+// at the team's barrier, and the stage's flag, which they read behind it, is not
+// written again before they have met once more.  (Until then only the stage of the
+// step before is refilled, whose copies are in.)  Nothing more is issued; what was, from
+// the stage that took too long on, is waited for here, again for a limited time, so
+// that no copy is on its way to the shared memory of a CTA that is gone.  The call then
+// ends with wrong results and FA_PAGED_TIMEOUT.  `stage` and `parity` are those of
+// the stage behind it.
+constexpr long long kDrainNs = 2000000000LL;
+__device__ __noinline__ void drain(uint32_t full, int stages, int fifo_what, int stage,
+                                   uint32_t parity) {
+  if (--stage < 0) {
+    stage = stages - 1;
+    parity ^= 1;
+  }
+  for (int i = 0; i < stages; ++i) {
+    if (__shfl_sync(kFull, fifo_what, stage) & kDone) break;   // nor any behind it
+    wait_phase(full + stage * 8, parity, kDrainNs, nullptr);
+    if (++stage == stages) {
+      stage = 0;
+      parity ^= 1;
+    }
+  }
 }
 
 // All warps of a team.
@@ -787,6 +824,7 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   __shared__ Partials<NT, R> s_part;
   __shared__ uint64_t s_full[NT][S];
   __shared__ int s_abort;
+  __shared__ volatile uint8_t s_gave_up[TW > 1 ? NT : 1][S];   // see drain
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / TW;
   const int row0 = warp % TW * RW;  // first row of the team's that is the warp's
   uint8_t *my = smem + team * Sh::kRing;
@@ -801,6 +839,7 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
       sm103::tma_prefetch_map(&maps.k);
       sm103::tma_prefetch_map(&maps.v);
       s_abort = 0;
+      for (int i = 0; TW > 1 && i < NT * S; ++i) s_gave_up[i / S][i % S] = 0;
       for (int i = 0; i < NT * S; ++i) sm103::mbar_init(sm103::smem_u32(&s_full[0][0] + i), TW);
       sm103::mbar_fence_init();
     }
@@ -832,15 +871,25 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   uint32_t qa[D / 16][2 * NR];
   float o[D / 8][4];
   float m[NR], l[NR];
-  bool opens = false;
+  bool opens = false, gave_up = false;
 
 #pragma unroll 1
   while (true) {
     if constexpr (!kTma) cp_async_wait<S - 2>();
     team_sync<TW>();                // the stage to fill has been read
+    if constexpr (kTma && TW == 1) gave_up = __any_sync(kFull, gave_up);
     const int what = __shfl_sync(kFull, load.fifo_what, stage);
-    if (what & kDone) break;
-    if constexpr (kTma) wait_stage(full + stage * 8, parity, &s_abort);
+    if ((what & kDone) || (TW == 1 && gave_up)) break;
+    if constexpr (kTma) {
+      if (!wait_phase(full + stage * 8, parity, p.wait_ns, &s_abort)) {
+        s_abort = 1;
+        if constexpr (TW == 1)
+          gave_up = true;
+        else
+          s_gave_up[team][stage] = 1;
+      }
+      if (TW > 1 && s_gave_up[team][fill]) break;
+    }
     const uint32_t kb = ring + stage * Sh::kStage, vb = kb + Sh::kBlock;
 
     if (what & kPartBegins) {
@@ -1067,17 +1116,16 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
       }
     }
   }
+  if constexpr (kTma && TW > 1) gave_up = s_gave_up[team][fill];
+  if (kTma && gave_up) {
+    load.err |= FA_PAGED_TIMEOUT;
+    drain(full, S, load.fifo_what, stage, parity);
+  }
   if (p.direct) {
     __syncthreads();
     float *cta_part = reinterpret_cast<float *>(smem + NT * Sh::kRing);
     merge_cta<T, D, R, Sh>(p, chunks, s_part, smem, cta_part);
     if (p.direct > 1) join_cluster<T, D, R, NW, NT, KB>(p, chunks, cta_part);
-  }
-  if constexpr (kTma) {
-    if (*static_cast<volatile int *>(&s_abort)) {
-      load.err |= FA_PAGED_TIMEOUT;
-      drain(full, S, stage, parity);
-    }
   }
   if (load.err && p.error) atomicOr(p.error, load.err);
 }
@@ -1149,16 +1197,19 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
   uint32_t parity = 0;
   float o[R][NV * VW], m[R], l[R];
   float4 q_own[kQRegs ? R : 1][kQRegs ? CPR / 4 : 1];
-  bool opens = false;
+  bool opens = false, gave_up = false;
 
 #pragma unroll 1
   while (true) {
     if constexpr (!kTma) cp_async_wait<S - 2>();
     __syncwarp();                    // the stage to fill has been read
+    if constexpr (kTma) gave_up = __any_sync(kFull, gave_up);
     const int what = __shfl_sync(kFull, load.fifo_what, stage);
-    if (what & kDone) break;
+    if ((what & kDone) || gave_up) break;
     if (what & kPartBegins) id = __shfl_sync(kFull, load.fifo_id, stage);
-    if constexpr (kTma) wait_stage(full + stage * 8, parity, &s_abort);
+    if constexpr (kTma) {
+      if (!wait_phase(full + stage * 8, parity, p.wait_ns, &s_abort)) gave_up = s_abort = true;
+    }
     uint8_t *kb = my + stage * Sh::kStage, *vb = kb + Sh::kBlock;
     load.issue(fill, ring + fill * Sh::kStage, full + fill * 8, q_places);
     load.look();
@@ -1315,17 +1366,15 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
         s_part.state[warp] = kHas | (opens ? kSegBegins : 0) | (ends ? kSegEnds : 0);
     }
   }
+  if (kTma && gave_up) {
+    load.err |= FA_PAGED_TIMEOUT;
+    drain(full, S, load.fifo_what, stage, parity);
+  }
   if (p.direct) {
     __syncthreads();
     float *cta_part = reinterpret_cast<float *>(smem + NW * Sh::kRing);
     merge_cta<float, D, R, Sh>(p, chunks, s_part, smem, cta_part);
     if (p.direct > 1) join_cluster<float, D, R, NW, NW, KB>(p, chunks, cta_part);
-  }
-  if constexpr (kTma) {
-    if (*static_cast<volatile int *>(&s_abort)) {
-      load.err |= FA_PAGED_TIMEOUT;
-      drain(full, S, stage, parity);
-    }
   }
   if (load.err && p.error) atomicOr(p.error, load.err);
 }
