@@ -521,7 +521,8 @@ fa_status fa_paged_decode_workspace_size(int64_t batch, int64_t head_num, int64_
  * position seq_lens[b] - 1 and sees the keys j < seq_lens[b] with
  * j >= seq_lens[b] - 1 - pre_tokens (its own among them: write the step's rows
  * first).  Formulas, grouped heads, types and head dims are those of
- * fa_varlen_fwd; pre_tokens likewise.
+ * fa_varlen_fwd; pre_tokens likewise.  scale * log2(e) has to be finite in
+ * fp32 (FA_ERR_INVALID otherwise); q . k is computed in fp32 before it is scaled.
  *   y             [batch, head_num, head_dim], rows y_stride elements apart
  *   softmax_max, softmax_sum: float32 [batch, head_num, 8], all lanes
  *                 written, as fa_varlen_fwd writes them; or both NULL

@@ -57,7 +57,7 @@ struct DecodeParams {
   int rows, direct;   // DecodePlan
   int ranges;         // teams of the main kernel
   int unit_shift;     // log2 of the blocks in a unit of work
-  float scale, scale_log2;
+  float scale_log2;
   long long wait_ns;  // bound on every in-kernel wait
 };
 

@@ -1,6 +1,7 @@
 // Host side of the paged-cache entry points: argument checks, the decode
 // workspace and the launches.  Nothing here allocates or throws.
 
+#include <cfloat>
 #include <cmath>
 
 #include "internal.h"
@@ -243,7 +244,9 @@ fa_status fa_paged_decode_ex(const fa_paged_decode_args *args,
   st = check_cache(a.k_pages, a.v_pages, a.num_pages, a.page_size, a.head_num_kv, a.head_dim,
                    page_stride, token_stride, head_stride, dtype);
   if (st != FA_OK) return st;
-  if (!std::isfinite(a.scale)) return FA_ERR_INVALID;
+  // The kernels hold it in 32 bits, where a larger one would make scores of 0 NaN.
+  const double scale_log2 = a.scale * 1.4426950408889634;
+  if (!(std::fabs(scale_log2) <= FLT_MAX)) return FA_ERR_INVALID;
   const int64_t row = a.head_num * a.head_dim;
   if (bad_rows(q_stride, a.batch, row) || bad_rows(y_stride, a.batch, row))
     return FA_ERR_INVALID;
@@ -294,8 +297,7 @@ fa_status fa_paged_decode_ex(const fa_paged_decode_args *args,
                q_stride % (dtype == FA_DTYPE_FP32 ? 4 : 8) == 0;
   p.y_pairs = pairs(a.y, y_stride);
   p.pre = int(a.pre_tokens < -1 ? -1 : a.pre_tokens > kMaxKeys ? kMaxKeys : a.pre_tokens);
-  p.scale = float(a.scale);
-  p.scale_log2 = float(a.scale * 1.4426950408889634);
+  p.scale_log2 = float(scale_log2);
   p.wait_ns = options && options->wait_timeout_ns > 0 ? options->wait_timeout_ns : kDefaultWaitNs;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == FA_DTYPE_FP32   ? launch_paged_decode_fp32(p, sms, cs)
