@@ -606,6 +606,8 @@ def paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, pre_tokens=2
             return paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, pre_tokens, y,
                                 stats, softmax_max, softmax_sum, workspace, error,
                                 wait_timeout_ns=wait_timeout_ns)
+    # A number: whatever else names one may change between calls.
+    pre_tokens = min(max(int(pre_tokens), -1), 2 ** 40)
     shape, strides = _pages(k_pages, v_pages, index)
     max_pages, table_stride = _table(block_table, index)
     b, heads, (_, _, n_kv, d) = block_table.size(0), q.shape, shape
@@ -644,7 +646,7 @@ def paged_decode(q, k_pages, v_pages, block_table, seq_lens, scale, pre_tokens=2
         q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), shape[0], shape[1], strides[0],
         strides[1], strides[2], block_table.data_ptr(), max_pages, table_stride,
         _flat(seq_lens, torch.int32, b, index, "seq_lens"), b, n, n_kv, d, _DTYPE[dtype], 0, scale,
-        min(max(int(pre_tokens), -1), 2 ** 40), y.data_ptr(), ys, top, total,
+        pre_tokens, y.data_ptr(), ys, top, total,
         0 if error is None else _flat(error, torch.int32, 1, index, "error"), at_workspace, nbytes)
     if wait_timeout_ns:
         status = lib().fa_paged_decode_ex(args, _pack_options(int(wait_timeout_ns)),
