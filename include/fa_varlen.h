@@ -377,14 +377,18 @@ fa_status fa_varlen_bwd_schedule_ex(const int64_t *seq_lens_q, const int64_t *se
  * a row's first max_pages entries count: key j of request b is token
  * j % page_size of page block_table[b, j / page_size].  Entries behind a
  * request's last page are never read.  Requests may share pages that
- * nobody writes.  seq_lens: int32 [batch] on the device, the keys that each
+ * nobody writes; fa_paged_plan knows nothing of that: it hands out slots in a
+ * request's half-filled last page, and gives back each page that a request
+ * loses, so a page in two rows must be full, and at most one of the rows may
+ * shrink past it.  seq_lens: int32 [batch] on the device, the keys that each
  * request holds.
  *
  * Everything that a call reads beyond its scalars is on the device, so the
  * calls of a decoding step can be captured once into a CUDA graph and
- * replayed; nothing synchronises.  What the host cannot check, the kernels
- * do: they add bits to *error (device int32, or NULL), which they never
- * clear, and read or write no memory through a bad value:
+ * replayed; nothing synchronises.  Lengths, tables and rows that a call reads
+ * must not change while it runs (on its own stream they cannot).  What the host
+ * cannot check, the kernels do: they add bits to *error (device int32, or NULL),
+ * which they never clear, and read or write no memory through a bad value:
  *   FA_PAGED_EXHAUSTED   plan: the free pages did not suffice for a request
  *   FA_PAGED_ROW_FULL    plan: a request would pass max_pages pages
  *   FA_PAGED_ROWS        plan: a request's new rows pass max_tokens
@@ -529,9 +533,15 @@ fa_status fa_paged_decode_workspace_size(int64_t batch, int64_t head_num, int64_
  * A request with no key to see (length 0, or pre_tokens < 0), or whose every
  * score is -inf, gets y = 0, max = -inf, sum = 0.  What the cache holds behind
  * a request's length, infinities and NaN too, has no influence.  (An infinite
- * value among the keys that count makes its column infinite in fp32, and infinite
- * or NaN in fp16 and bf16, whose weights are multiplied in two parts.)  The result does not
- * change from run to run on one device (fixed add order).
+ * value among the keys that count makes its column infinite in fp32, or NaN where
+ * its key's weight is too small for fp32; in fp16 and bf16, whose weights are
+ * multiplied in two parts, infinite or NaN.)  The result does not change from run
+ * to run on one device (fixed add order).
+ * How a call is run follows from its scalars.  Where batch, heads and max_pages (or
+ * pre_tokens) allow few and short requests only, each is finished by one CTA or
+ * cluster, without workspace and second kernel; so pass a table no wider than the
+ * requests of the moment need (a view of a wider one: table_stride), for instance
+ * one graph each for widths that double.
  * workspace: 16-byte aligned (FA_ERR_INVALID otherwise), at least what
  * fa_paged_decode_workspace_size gives; NULL where that is 0. */
 fa_status fa_paged_decode(const fa_paged_decode_args *args, fa_stream_t stream);

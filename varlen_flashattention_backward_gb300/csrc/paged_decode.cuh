@@ -22,7 +22,8 @@ constexpr uint32_t kFull = 0xffffffffu;
 // with 0, 15.1 with 1).
 constexpr int kSwitchBlocks = 1;
 // Most CTAs of a cluster that shares a segment, and blocks for each team of it (16
-// requests of 512 keys, 8 key heads: 8.7 us so, 13.0 by ranges).
+// requests of 512 keys, 8 key heads: 8.9 us so, 11.7 by ranges; one of 8000 keys 14.6
+// and 12.5).
 constexpr int kMaxDirect = 8;
 constexpr int kDirectBlocks = 8;
 
@@ -118,7 +119,7 @@ __device__ __forceinline__ int units_at(const DecodeParams &p, int b, bool &bad)
 }
 
 // Measures the line and finds unit `start(range) - before` on it.  Every warp
-// that asks works it out for itself from all lengths: that costs less than
+// of the main kernel works it out for itself from all lengths: that costs less than
 // meeting other warps would.  Lane i sums up requests 32 i .. 32 i + 31 (and
 // those 1024 further on), then the warp looks at the 32 that hold the unit.
 // False: nothing is there.  (The indexes are held in bounds for the sake of
@@ -222,7 +223,7 @@ enum : int {
 // part and EXTRA bytes more.  In the end the sum of the whole CTA takes the place
 // behind the rings.  Query rows are fetched ahead where that leaves three stages:
 // under load a fetch takes 1 to 2 us, which a warp would spend waiting at each of its
-// parts (1024 requests of 64 keys, 32 / 8 heads, D 128: 91 us without, 75 with).
+// parts (1024 requests of 64 keys, 32 / 8 heads, D 128: 16 us more without).
 template <typename T, int D, int RW, int TW, int KB, int EXTRA, int WARPS>
 struct Shape {
   static constexpr int R = RW * TW;
@@ -811,13 +812,18 @@ using TcShape = Shape<__half, D, TcTeam<R>::RW, TcTeam<R>::TW, 16, 0, tc_warps(D
 // Bound by memory for a few query heads per key head: each key is read once, for
 // 4 R operations per element.  One CTA of 4 to 16 warps per SM, each with a ring of its
 // own, because what keeps HBM busy is bytes on the way (150 to 200 KB per SM) and no
-// warp has to meet another; mma.sync rather than tcgen05, because 8 or 16 rows
-// would fill an eighth of the latter's 128.  64 requests of 2048 keys, 32 / 8 heads,
-// D 128, bf16: 89 us, 6.0 TB/s, 26% of the issue slots; a warp waits for its copies
-// and for latencies (products, exponentials, shuffles) in equal parts.  From about
-// 16 rows the products' latency bounds it (32 requests of 2000 to 8192 keys, 32 heads
-// on one, D 192: 39 us, 107 TFLOP/s).  Not faster: a warp that only loads, K and V awaited apart, ranges
-// taken from a counter.
+// warp has to meet another.  64 requests of 2048 keys, 32 / 8 heads,
+// D 128, bf16: 90 us, 6.0 TB/s, 26% of the issue slots; a warp waits for its copies
+// and for latencies (products, exponentials, shuffles) in equal parts.  At D 32 and 64 a
+// block of 16 keys is so few bytes that what a warp does once per block bounds it (64
+// requests of 4000 keys, 8 / 8 heads, D 32: 93 us for 39 us of bytes; 32 / 4, D 64: 57 for
+// 39), and from about 16 rows the products' latency does (32 requests of 2000 to 8192 keys,
+// 32 heads on one, D 192: 38 us, 108 TFLOP/s; 32 of 5000, 64 on one, D 128: 51 us for 12).
+//
+// mma.sync: with up to 16 query heads per key head the heads fill 8 or 16 of the 128 rows
+// that tcgen05 multiplies at once.  With more heads, or with keys for rows, tcgen05
+// would fit; such a kernel has not been built.  Not faster: a warp that only loads,
+// K and V awaited apart, ranges taken from a counter.
 template <typename T, int D, int R, bool kTma>
 __global__ void __launch_bounds__(TcShape<D, R>::NW * 32, 1)
 decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ DecodeMaps maps) {
@@ -1394,7 +1400,7 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
 // so that their loads overlap, and meet in shared memory, always in the same order.
 // Bound by latency: a chain of two dependent loads (lengths, parts) and the launch,
 // of which the first and the last hide behind the main kernel.  About 3 us of a call
-// that is cut (16 requests of 512 keys: 13.0 us, of which 8.7 remain without the join
+// that is cut (16 requests of 512 keys: 11.7 us, of which 8.9 remain without the join
 // and the search for ranges).
 // ---------------------------------------------------------------------------
 template <typename T, int D, int KB, int WPR>

@@ -51,10 +51,11 @@ DecodePlan decode_plan(fa_dtype dt, int batch, int n_kv, int group, int d, int64
   // The largest cluster per segment that still puts all of them on the GPU at
   // once, if its teams get at most kDirectBlocks blocks each.  Clusters share a
   // GPC, so fewer large ones fit than SMs would hold (152 SMs: 15 of eight, 36 of
-  // four, 76 of two); a second wave doubles the time.  Of single CTAs, two waves: they
-  // take the GPU what ranges and a join take (61 requests of up to 128 keys, 4 key heads
-  // 8.9 us and 9.8; 32 of up to 512, 8 key heads 14.5 and 13.7; 32 of 512 16.2 and 16.6),
-  // and the host 4 us less, for a launch and a workspace.
+  // four, 76 of two); a second wave doubles the time.  Of single CTAs, two waves: on the
+  // GPU they take 1.6 us less than ranges and a join to 1.8 us more (61 requests of up to
+  // 128 keys, 4 key heads 8.8 us and 10.4; 32 of up to 512, 8 key heads 13.8 and 12.0; 32
+  // of 512 16.3 and 15.2), but the host saves a launch and a workspace: calls on a stream
+  // take 8.6 and 18.6, 13.7 and 18.3, 16.2 and 19.2 us.
   const int kb = tc ? 16 : 8;
   const int64_t blocks = (max_keys + kb - 1) / kb + 1;
   const int64_t segments = int64_t(batch) * n_kv * ((group + plan.rows - 1) / plan.rows);
