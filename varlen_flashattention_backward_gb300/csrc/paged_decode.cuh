@@ -235,7 +235,8 @@ struct Shape {
   // The kernels' static arrays, in the steps of the ring's alignment.
   static constexpr int static_bytes(int nw, int s) {
     const int nt = nw / TW;
-    return (nt * (R * 8 + 4) + nt * s * 8 + 64 + 1023) / 1024 * 1024;
+    return (nt * (R * 8 + 4) + nt * s * (TW > 1 ? 9 : 8) + (TW > 1 ? nt * 24 : 0) + 64 + 1023) /
+           1024 * 1024;
   }
   // Most stages, up to 8, that fit.
   static constexpr int fit(int nw, int qs) {
@@ -292,9 +293,23 @@ __device__ __forceinline__ void tma_load_panels_w(uint32_t dst_k, uint32_t dst_v
       : "memory");
 }
 
+// All warps of a team.
+template <int TW>
+__device__ __forceinline__ void team_sync() {
+  if constexpr (TW == 1) {
+    __syncwarp();
+  } else {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + int(threadIdx.x >> 5) / TW), "n"(32 * TW)
+                 : "memory");
+  }
+}
+
 // The loading side of a team: walks its range and keeps the ring filled.
 // `look` finds the next block, `issue`, one block later, starts its copies.  All
-// warps of the team walk alike.  With pages of whole blocks (kTma) one lane starts
+// warps of the team walk alike, and meet at barriers on the strength of that; so one
+// reads the lengths for all (`common`: two places for a length, in turn, and the range's
+// beginning), and not even lengths that change during the call can part them.
+// With pages of whole blocks (kTma) one lane starts
 // TMA copies of whole panels, and the lanes hold the page ids of 32 blocks; else
 // the lanes copy 16 bytes at a time, each warp its share, and hold the pages of
 // their rows.  This runs once per block in a warp that has but one other to hide
@@ -324,18 +339,21 @@ struct Loader {
   int err;
   int parts, parts_free;         // begun so far, and how many hold no query place any more
   int fifo_what, fifo_id;        // lane i: the block in stage i
+  volatile int *const common;    // of teams of several warps
+  int entered;                   // requests entered so far
 
-  __device__ __forceinline__ Loader(const DecodeParams &p, const DecodeMaps &maps, int chunks)
+  __device__ __forceinline__ Loader(const DecodeParams &p, const DecodeMaps &maps, int chunks,
+                                    volatile int *common)
       : p(p), maps(maps), chunks(chunks), segs(p.n_kv * chunks), lane(threadIdx.x & 31),
         member((threadIdx.x >> 5) % TW), left(0), off(0), units(1), b(0), seg(0), blk(0), end(0),
         what(0), block_b(0), head(0), row(0), tok(0), id(0), page(-1), page_lane(0), err(0),
-        parts(0), parts_free(0), fifo_what(kDone), fifo_id(0) {
+        parts(0), parts_free(0), fifo_what(kDone), fifo_id(0), common(common), entered(0) {
     const int team = (threadIdx.x >> 5) / TW;
     if (p.direct) {
       const int cta = blockIdx.x / p.direct, teams = p.direct * Sh::NT;
       b = cta / segs;
       seg = cta - b * segs;
-      const int len = length_of(p, b);
+      const int len = common_length();
       if ((len < 0 || len > p.max_pages * p.page_size) && p.error)
         atomicOr(p.error, FA_PAGED_BAD_LENGTH);
       // Its share as a range whose units are blocks.
@@ -348,20 +366,51 @@ struct Loader {
       return;
     }
     const int range = blockIdx.x * Sh::NT + team;
-    Line line;
-    Place at;
-    if (find<KB, false>(p, segs, range, 0, line, at)) {
-      left = line.each + (range < line.rest ? 1 : 0);
-      b = at.b;
-      seg = at.seg;
+    if (TW == 1 || member == 0) {
+      Line line;
+      Place at;
+      if (find<KB, false>(p, segs, range, 0, line, at)) {
+        left = line.each + (range < line.rest ? 1 : 0);
+        b = at.b;
+        seg = at.seg;
+        off = at.off;
+      }
+    }
+    if constexpr (TW > 1) {
+      if (member == 0) {
+        common[2] = left;
+        common[3] = b;
+        common[4] = seg;
+        common[5] = off;
+      }
+      team_sync<TW>();
+      left = common[2];
+      b = common[3];
+      seg = common[4];
+      off = common[5];
+    }
+    if (left > 0) {
       enter();
-      off = min(at.off, units - 1);
+      off = min(off, units - 1);
+    }
+  }
+
+  // Request b's length, as one warp of the team reads it.  (A place is written again
+  // two requests later, when all have met in between.)
+  __device__ __forceinline__ int common_length() {
+    if constexpr (TW == 1) {
+      return length_of(p, b);
+    } else {
+      const int at = entered++ & 1;
+      if (member == 0) common[at] = length_of(p, b);
+      team_sync<TW>();
+      return common[at];
     }
   }
 
   // Request b's span (its segments have the same).
   __device__ __forceinline__ void enter() {
-    span = span_of<KB>(p, length_of(p, b));
+    span = span_of<KB>(p, common_length());
     units = units_of(p, span.blocks);
   }
 
@@ -576,17 +625,6 @@ __device__ __noinline__ void drain(uint32_t full, int stages, int fifo_what, int
       stage = 0;
       parity ^= 1;
     }
-  }
-}
-
-// All warps of a team.
-template <int TW>
-__device__ __forceinline__ void team_sync() {
-  if constexpr (TW == 1) {
-    __syncwarp();
-  } else {
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + int(threadIdx.x >> 5) / TW), "n"(32 * TW)
-                 : "memory");
   }
 }
 
@@ -838,6 +876,7 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   __shared__ uint64_t s_full[NT][S];
   __shared__ int s_abort;
   __shared__ volatile uint8_t s_gave_up[TW > 1 ? NT : 1][S];   // see drain
+  __shared__ volatile int s_common[TW > 1 ? NT : 1][6];        // see Loader
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / TW;
   const int row0 = warp % TW * RW;  // first row of the team's that is the warp's
   uint8_t *my = smem + team * Sh::kRing;
@@ -864,7 +903,7 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // The join reads the lengths as soon as it runs, so it may not before this.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Loader<T, D, Sh, RW, TW, KB, kTma> load(p, maps, chunks);
+  Loader<T, D, Sh, RW, TW, KB, kTma> load(p, maps, chunks, s_common[TW > 1 ? team : 0]);
   load.look();
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) {
@@ -969,8 +1008,9 @@ decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
     }
     const int mask = what & 0xffff;
     if (kTma && mask != 0xffff) {
+      // Each warp of the team clears them all, so none waits for another.
       clear_rows<D * 2, KB>(my + (vb - ring), mask);
-      team_sync<TW>();
+      __syncwarp();
     }
 
     float sa[2][2][4];              // [chain][key half][fragment]
@@ -1197,7 +1237,7 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p,
 
   asm volatile("griddepcontrol.wait;" ::: "memory");   // as above
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Loader<float, D, Sh, R, 1, KB, kTma> load(p, maps, chunks);
+  Loader<float, D, Sh, R, 1, KB, kTma> load(p, maps, chunks, nullptr);
   load.look();
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) {
