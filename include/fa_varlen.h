@@ -408,7 +408,8 @@ fa_status fa_varlen_bwd_schedule_ex(const int64_t *seq_lens_q, const int64_t *se
  *                        whose row is skipped
  * Limits (FA_ERR_INVALID): batch in [1, 2048]; num_pages in [1, 2^31);
  * page_size in [1, 65536]; max_pages >= 1 with max_pages * page_size <= 2^30;
- * table_stride >= max_pages.  Head counts and dims as above.
+ * table_stride >= max_pages; every address aligned to its type.  Head counts
+ * and dims as above.
  * ------------------------------------------------------------------------- */
 enum {
   FA_PAGED_EXHAUSTED = 1,

@@ -92,6 +92,12 @@ bool element_aligned(const void *ptr, fa_dtype dt) {
   return reinterpret_cast<uintptr_t>(ptr) % (dt == FA_DTYPE_FP32 ? 4 : 2) == 0;
 }
 
+// Whole numbers and statistics: aligned to their type (NULL is).
+template <typename... Ptr>
+bool misaligned(const Ptr *...ptr) {
+  return (... || (reinterpret_cast<uintptr_t>(ptr) % sizeof(Ptr) != 0));
+}
+
 // log2 of a power of 2, -1 for another number.
 int log2_or_none(int64_t x) {
   if ((x & (x - 1)) != 0) return -1;
@@ -132,6 +138,9 @@ fa_status fa_paged_plan(const fa_paged_plan_args *args, fa_stream_t stream) {
       check_table(a.batch, a.num_pages, a.page_size, a.max_pages, a.table_stride);
   if (st != FA_OK) return st;
   if (a.max_tokens < 0 || a.max_tokens > kMaxI32) return FA_ERR_INVALID;
+  if (misaligned(a.block_table, a.seq_lens, a.delta, a.free_pages, a.free_state, a.slots,
+                 a.cu_tokens, a.seq_lens_out, a.free_state_out, a.error))
+    return FA_ERR_INVALID;
   PlanParams p{};
   p.table = a.block_table;
   p.table_stride = a.table_stride;
@@ -177,7 +186,9 @@ fa_status fa_paged_write(const fa_paged_write_args *args, fa_stream_t stream) {
   const int64_t row = a.head_num_kv * a.head_dim;
   if (bad_rows(k_stride, a.tokens, row) || bad_rows(v_stride, a.tokens, row))
     return FA_ERR_INVALID;
-  if (!element_aligned(a.k, dtype) || !element_aligned(a.v, dtype)) return FA_ERR_INVALID;
+  if (!element_aligned(a.k, dtype) || !element_aligned(a.v, dtype) ||
+      misaligned(a.slots, a.error))
+    return FA_ERR_INVALID;
   if (a.tokens == 0) return FA_OK;
   WriteParams p{};
   p.k = a.k;
@@ -250,7 +261,9 @@ fa_status fa_paged_decode_ex(const fa_paged_decode_args *args,
   const int64_t row = a.head_num * a.head_dim;
   if (bad_rows(q_stride, a.batch, row) || bad_rows(y_stride, a.batch, row))
     return FA_ERR_INVALID;
-  if (!element_aligned(a.q, dtype) || !element_aligned(a.y, dtype)) return FA_ERR_INVALID;
+  if (!element_aligned(a.q, dtype) || !element_aligned(a.y, dtype) ||
+      misaligned(a.block_table, a.seq_lens, a.softmax_max, a.softmax_sum, a.error))
+    return FA_ERR_INVALID;
   const int sms = sm_count();
   const int group = int(a.head_num / a.head_num_kv);
   const DecodePlan plan =
