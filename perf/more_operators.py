@@ -346,8 +346,6 @@ def prepare(c, seed):
              "free_state": pool, "error": error}
     if c["op"] == "fork":
         state["source"] = torch.from_numpy(_sources(c)).to(DEV)
-    else:
-        state["new_pages"] = _pool(c)[1]
     return state
 
 
@@ -503,7 +501,7 @@ def run(s):
         return (start, end, s["block_table"], s["seq_lens"], s["shares"], s["free_pages"],
                 s["free_state"], s["error"])
     start, end, table, ring, pool, shares = fa.paged_compact(
-        s["block_table"], s["seq_lens"], s["free_pages"], s["free_state"], c["page"], s["new_pages"],
+        s["block_table"], s["seq_lens"], s["free_pages"], s["free_state"], c["page"], _pool(c)[1],
         shares=s["shares"], error=s["error"])
     return start, end, table, ring, pool, shares, s["error"]
 
