@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // both have.
       constexpr int kChunks = D / 8;
       uint32_t freed[2] = {0, 0};        // how often each warpgroup has, or will have
-      uint32_t filled[2] = {0, 0};
+      uint32_t filled[2] = {0, 0};       // how often copies to each half have begun
       bool shared = false;
       for (uint32_t items = 0;; ++items) {
         const int slot = int(items % kItems);
@@ -550,6 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (freed[w] > 0) ok = wait(ctl, bar(c->query_free[w]), (freed[w] - 1) & 1);
           if (ok && w == 0 && shared) ok = wait(ctl, bar(c->query_free[1]), (freed[1] - 1) & 1);
           if (!ok) break;
+          ++filled[w];     // now: the other half's wait may give up while these copies are on the way
           const uint32_t dst = sq + w * M::kQ;
           if (maps.by_tma) {
             // 128 / group tokens and the group's heads are 128 packed rows; what lies behind
@@ -616,8 +617,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         shared = !it.both && it.steps > 1;
         ++freed[0];
         if (it.steps > 1) ++freed[1];
-        ++filled[0];
-        if (it.both) ++filled[1];
       }
       // No copy may still be writing shared memory when the CTA exits.
       cp_async_wait_all();
