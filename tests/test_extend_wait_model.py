@@ -96,3 +96,17 @@ def test_the_kernel_counts_a_half_before_it_is_filled():
     armed = text.index("mbar_arrive_expect_tx(bar(c->query[w]), M::kQ);")
     waits = text.rindex("if (!ok) break;", 0, armed)
     assert len(counted) == 1 and waits < counted[0] < armed
+
+
+def test_the_kernel_waits_for_every_phase_that_it_began():
+    # Whether its copies were TMA's or pieces, which the barrier counts in by an arrival of
+    # its own: the waits at the end make no difference.
+    with open(os.path.join(fb.CSRC, "paged_extend_tc.cuh")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    ends = re.findall(r"&never\)", text)
+    assert len(ends) == 3                       # K and V, the query rows, the MMAs
+    drain = text[text.index("void drain("):]
+    drain = drain[:drain.index("&never")]
+    assert "if (" not in drain
+    rows = text[text.index("if (filled[w] > 0)"):]
+    assert re.match(r"if \(filled\[w\] > 0\) mbar_wait\(", rows)

@@ -267,7 +267,6 @@ struct Loader {
   int lane, kv;                        // kv: 0 for K, 1 for V
   int err = 0;
   int tiles = 0;                       // so far
-  uint32_t by_tma = 0;                 // stages last filled by TMA
 
   __device__ __forceinline__ uint32_t bar(uint64_t &b) const { return smem_u32(&b); }
 
@@ -309,7 +308,6 @@ struct Loader {
     if (box && __all_sync(kFull, pages.of[0] >= 0 && pages.of[0] < p.num_pages)) {
       const int boxes = M::BN / maps.box, mine = lane & (boxes - 1);
       const int token = token_of(key0 + mine * maps.box);
-      by_tma |= 1u << place.stage;
       if (kv == 0 && lane < 4) c->mask[which][lane] = ~0u;
       __syncwarp();
       if (lane == 0) mbar_arrive_expect_tx(full, M::kStage);
@@ -326,7 +324,6 @@ struct Loader {
     // after the other.
     constexpr int kChunks = D / 8;
     constexpr int kAcross = kChunks <= 4 ? 4 : kChunks <= 8 ? 8 : kChunks <= 16 ? 16 : 32;
-    by_tma &= ~(1u << place.stage);
     const T *cache = static_cast<const T *>(kv ? p.vc : p.kc);
     const int ch = lane & (kAcross - 1), sub = lane / kAcross;
     const uint32_t dst = ring + place.stage * M::kStage + (ch >> 3) * M::kPanel;
@@ -381,13 +378,14 @@ struct Loader {
     return true;
   }
 
-  // No copy may still be writing shared memory when the CTA exits.
+  // No copy may still be writing shared memory when the CTA exits, nor the arrival that
+  // counts pieces in, which comes behind them.
   __device__ __forceinline__ void drain(long long ns) {
     cp_async_wait_all();
     const int never = 0, stages = kv ? M::kStagesV : M::kStagesK;
     for (int t = tiles > stages ? tiles - stages : 0; t < tiles; ++t) {
       const Stage at = place_of<D>(kv, t);
-      if ((by_tma >> at.stage) & 1) mbar_wait(bar(c->full[at.stage]), uint32_t(at.turn) & 1, ns, &never);
+      mbar_wait(bar(c->full[at.stage]), uint32_t(at.turn) & 1, ns, &never);
     }
     if (err && p.error) atomicOr(p.error, err);
   }
@@ -618,11 +616,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++freed[0];
         if (it.steps > 1) ++freed[1];
       }
-      // No copy may still be writing shared memory when the CTA exits.
+      // As Loader::drain.
       cp_async_wait_all();
       const int never = 0;
       for (int w = 0; w < 2; ++w)
-        if (maps.by_tma && filled[w] > 0) mbar_wait(bar(c->query[w]), (filled[w] - 1) & 1, drain_ns, &never);
+        if (filled[w] > 0) mbar_wait(bar(c->query[w]), (filled[w] - 1) & 1, drain_ns, &never);
     } else if (warp == 9) {
       // ---------------------------------------------------------------- MMA issuer
       const uint32_t id_s = idesc_f16(128, BN, false, false, kBF16);
