@@ -399,9 +399,8 @@ fa_status fa_varlen_bwd_schedule_ex(const int64_t *seq_lens_q, const int64_t *se
  *                        changes nothing
  *   FA_PAGED_ROW_FULL    plan: a request would pass max_pages pages
  *   FA_PAGED_ROWS        plan: a request's new rows pass max_tokens; extend: its
- *                        rows are not in [0, tokens], or not behind the request's
- *                        before it (they are cut; where more rows remain than there
- *                        are, the call does nothing)
+ *                        rows are not in [0, tokens] (they are cut), or cu_tokens
+ *                        descends (the call writes nothing else)
  *   FA_PAGED_BAD_PAGE    a page id outside [0, num_pages) in a place that
  *                        counts (plan: its slots become -1; decode, extend: its
  *                        keys take no part)

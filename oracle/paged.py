@@ -154,6 +154,7 @@ def paged_extend(q, k_pages, v_pages, block_table, seq_lens, cu_tokens, scale,
     top, total = np.full((tokens, heads), -np.inf), np.zeros((tokens, heads))
     weight, seen = np.zeros((tokens, heads)), np.zeros(tokens, np.int64)
     owned, error = np.zeros(tokens, bool), 0
+    descends = (np.diff(cu_tokens) < 0).any()      # requests could share rows: nothing is done
     for b in range(len(seq_lens)):
         start = min(max(int(cu_tokens[b]), 0), tokens)
         end = min(max(int(cu_tokens[b + 1]), start), tokens)
@@ -163,6 +164,8 @@ def paged_extend(q, k_pages, v_pages, block_table, seq_lens, cu_tokens, scale,
         if not 0 <= length <= most:
             error |= BAD_LENGTH
             length = min(max(length, 0), most)
+        if descends:
+            continue
         n = end - start
         owned[start:end] = True
         if n == 0:

@@ -119,7 +119,6 @@ struct ExtendParams {
   void *records;
   float *parts;
   uint32_t *flags;
-  int64_t most_blocks;   // blocks of one key head that the rows can make
   int num_pages, page_size, page_shift;   // page_shift: log2(page_size), or -1
   int max_pages, batch, tokens, n, n_kv, d, group;
   int pre, next;         // clamped to +-(2^30 - 1)
@@ -137,7 +136,7 @@ constexpr int kExtendRecord = 64;   // bytes of a CTA's record
 struct ExtendPlan {
   int rows;              // packed rows in a block
   int ctas;
-  int64_t most_blocks;
+  int64_t most_blocks;   // of one key head, that the rows can make
   size_t parts, flags, bytes;   // offsets (the records come first), and the end
 };
 ExtendPlan extend_plan(fa_dtype dt, int64_t batch, int64_t tokens, int n, int n_kv, int d, int sms);

@@ -315,7 +315,6 @@ fa_status fa_paged_extend_ex(const fa_paged_extend_args *args,
   p.records = work;
   p.parts = reinterpret_cast<float *>(work + plan.parts);
   p.flags = reinterpret_cast<uint32_t *>(work + plan.flags);
-  p.most_blocks = plan.most_blocks;
   p.num_pages = int(a.num_pages);
   p.page_size = int(a.page_size);
   p.page_shift = log2_or_none(a.page_size);

@@ -97,7 +97,6 @@ struct Place {
 struct Line {
   int64_t span;       // units per CTA
   int64_t units;      // in all
-  int blocks;         // in all, per key head
 };
 
 // Scratch of measure(), per CTA.
@@ -117,6 +116,7 @@ __device__ bool measure(const ExtendParams &p, Measure &m, Line &line, Place &at
   constexpr int kLanes = 8;      // that share a request's blocks
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int err = 0;
+  bool descends = false;
 #pragma unroll 1
   for (int b0 = 0; b0 < p.batch; b0 += THREADS / kLanes) {
     const int b = b0 + tid / kLanes;
@@ -124,6 +124,7 @@ __device__ bool measure(const ExtendParams &p, Measure &m, Line &line, Place &at
     int n = 0;
     if (b < p.batch) {
       const Request r = request_of(p, b, err);
+      descends |= p.cu[b + 1] < p.cu[b];
       if (tid % kLanes == 0) m.request[b] = r;
       n = blocks_of<BR>(p, r);
 #pragma unroll 1
@@ -137,10 +138,15 @@ __device__ bool measure(const ExtendParams &p, Measure &m, Line &line, Place &at
     }
   }
   if (err && blockIdx.x == 0 && p.error) atomicOr(p.error, err);
-  __syncthreads();
+  // Requests whose bounds descend could share rows: nothing is done then.  (Ascending ones
+  // have rows of their own, so that no more blocks come together than the workspace has
+  // flags for.)
+  line = Line{};
+  if (__syncthreads_or(descends)) return false;
   // Prefix sums: each thread a run of requests, each warp, all warps.
   const int per = (p.batch + THREADS - 1) / THREADS;
-  int64_t own = 0, own_blocks = 0;
+  int64_t own = 0;
+  int own_blocks = 0;
 #pragma unroll 1
   for (int k = 0; k < per; ++k) {
     const int b = tid * per + k;
@@ -149,10 +155,12 @@ __device__ bool measure(const ExtendParams &p, Measure &m, Line &line, Place &at
       own_blocks += m.blocks[b + 1];
     }
   }
-  int64_t x = own, y = own_blocks;
+  int64_t x = own;
+  int y = own_blocks;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(kFull, x, o), v = __shfl_up_sync(kFull, y, o);
+    const int64_t u = __shfl_up_sync(kFull, x, o);
+    const int v = __shfl_up_sync(kFull, y, o);
     if (lane >= o) {
       x += u;
       y += v;
@@ -161,10 +169,11 @@ __device__ bool measure(const ExtendParams &p, Measure &m, Line &line, Place &at
   __syncthreads();
   if (lane == 31) {
     m.sum64[warp] = x;
-    m.sum32[warp] = int(min(y, int64_t(1) << 30));
+    m.sum32[warp] = y;
   }
   __syncthreads();
-  int64_t before = x - own, before_blocks = y - own_blocks, all = 0, all_blocks = 0;
+  int64_t before = x - own, all = 0;
+  int before_blocks = y - own_blocks;
 #pragma unroll 1
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) {
@@ -172,7 +181,6 @@ __device__ bool measure(const ExtendParams &p, Measure &m, Line &line, Place &at
       before_blocks += m.sum32[w];
     }
     all += m.sum64[w];
-    all_blocks += m.sum32[w];
   }
 #pragma unroll 1
   for (int k = 0; k < per; ++k) {
@@ -181,7 +189,7 @@ __device__ bool measure(const ExtendParams &p, Measure &m, Line &line, Place &at
       before += m.upto[b + 1];
       before_blocks += m.blocks[b + 1];
       m.upto[b + 1] = before;
-      m.blocks[b + 1] = int(min(before_blocks, int64_t(1) << 30));
+      m.blocks[b + 1] = before_blocks;
     }
   }
   if (tid == 0) {
@@ -190,14 +198,6 @@ __device__ bool measure(const ExtendParams &p, Measure &m, Line &line, Place &at
   }
   __syncthreads();
   line.units = all * p.n_kv;
-  line.blocks = int(min(all_blocks, int64_t(1) << 30));
-  // More blocks than rows that do not overlap can have: nothing is done (the rows'
-  // bounds were not in ascending order).
-  if (all_blocks > p.most_blocks) {
-    if (blockIdx.x == 0 && tid == 0 && p.error) atomicOr(p.error, FA_PAGED_ROWS);
-    line.units = 0;
-    line.blocks = 0;
-  }
   line.span = max((line.units + gridDim.x - 1) / gridDim.x, int64_t(p.least_span));
   at.at = line.span * blockIdx.x;
   at.left = min(line.span, line.units - at.at);
