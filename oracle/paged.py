@@ -175,6 +175,7 @@ def paged_extend(q, k_pages, v_pages, block_table, seq_lens, cu_tokens, scale,
         hi = np.maximum(np.clip(pos + next_tokens + 1, 0, length), lo)
         first, last = int(lo.min()), int(hi.max())
         j = np.arange(first, max(first, last))
+        j = j[((j >= lo[:, None]) & (j < hi[:, None])).any(0)]      # (none between empty windows)
         pages = np.asarray(block_table[b], np.int64)[j // page_size]
         fine = (pages >= 0) & (pages < num_pages)
         if not fine.all():

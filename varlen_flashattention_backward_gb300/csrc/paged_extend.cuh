@@ -64,6 +64,7 @@ __device__ __forceinline__ void keys_of(const ExtendParams &p, const Request &r,
 struct Block {
   int row0, rows;      // its packed rows
   int tile0, tiles;    // the keys' tiles that any of them may see
+  int lo, hi;          // the keys that any of them sees
 };
 
 template <int BR, int BN>
@@ -71,11 +72,14 @@ __device__ __forceinline__ Block block_of(const ExtendParams &p, const Request &
   Block k;
   k.row0 = i * BR;
   k.rows = min(BR, r.n * p.group - k.row0);
-  int lo, hi, unused;
-  keys_of(p, r, k.row0 / p.group, lo, unused);
+  int hi, unused;
+  keys_of(p, r, k.row0 / p.group, k.lo, unused);
   keys_of(p, r, (k.row0 + k.rows - 1) / p.group, unused, hi);
-  k.tile0 = lo / BN;
-  k.tiles = hi > lo ? (hi + BN - 1) / BN - k.tile0 : 0;
+  k.tile0 = k.lo / BN;
+  k.tiles = hi > k.lo ? (hi + BN - 1) / BN - k.tile0 : 0;
+  // Windows of neighbouring rows lie one key apart, so that together they leave no gap;
+  // where they are empty, what lies between two of them is nobody's.
+  k.hi = p.pre + p.next < 0 ? k.lo : hi;
   return k;
 }
 

@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, D <= 64 ? 3 : 2) extend_fp32_kernel(
       const float *src = j < r.len ? cached<float>(p, cache, seg.b, seg.h, j) : nullptr;
       if (fine != nullptr && part == 0) {
         fine[key] = src != nullptr;
-        if (j < r.len && src == nullptr) err |= FA_PAGED_BAD_PAGE;
+        if (j >= seg.k.lo && j < seg.k.hi && src == nullptr) err |= FA_PAGED_BAD_PAGE;
       }
       const float *from = src != nullptr ? src : static_cast<const float *>(cache);
 #pragma unroll

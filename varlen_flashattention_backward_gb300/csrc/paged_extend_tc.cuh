@@ -104,6 +104,7 @@ __device__ __forceinline__ Stage place_of(int kv, int tile) {
 struct Item {
   Request r;
   int row0, rows;      // packed rows
+  int lo, hi;          // the keys that any of them sees
   int b, h, key0, steps;  // first key of its first tile; turns of a softmax warpgroup, both together
   int both;            // the halves have rows of their own
   int tile;            // number of its first tile in the CTA
@@ -267,6 +268,7 @@ struct Loader {
   int lane, kv;                        // kv: 0 for K, 1 for V
   int err = 0;
   int tiles = 0;                       // so far
+  int lo = 0, hi = 0;                  // the keys of the segment that any row sees
 
   __device__ __forceinline__ uint32_t bar(uint64_t &b) const { return smem_u32(&b); }
 
@@ -341,7 +343,7 @@ struct Loader {
       if (key < len) {
         if (page >= 0 && page < p.num_pages)
           at = page * p.page_stride + token_of(key) * p.token_stride + h * p.head_stride;
-        else
+        else if (key >= lo && key < hi)
           err |= FA_PAGED_BAD_PAGE;
       }
       const uint32_t word = __ballot_sync(kFull, at >= 0);
@@ -500,6 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               it.r = seg.r;
               it.row0 = seg.k.row0;
               it.rows = seg.k.rows;
+              it.lo = seg.k.lo;
+              it.hi = seg.k.hi;
               it.b = seg.b;
               it.h = seg.h;
               it.key0 = (seg.k.tile0 + seg.t0) * BN;
@@ -517,6 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const int len = it.r.len, b = it.b, h = it.h, key0 = it.key0, end = it.end, count = it.steps >> it.both;
+        load.lo = it.lo;
+        load.hi = it.hi;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(c->item_empty[slot]));
         if (end || !load.all(len, b, h, key0, count)) break;
