@@ -646,7 +646,8 @@ fa_status fa_paged_decode_ex(const fa_paged_decode_args *args,
  * rows are written first, and seq_lens counts them).
  * Formulas, grouped heads, types and head dims are those of fa_varlen_fwd; scale as for
  * fa_paged_decode.  Weights are rounded to the type before they meet the values (fp16:
- * times 2^7); their sum is taken in fp32 before that.
+ * times 2^7; bf16: times 2^-8, so that none passes 1); their sum is taken in fp32
+ * before that, and the values' in fp32 too.
  *   y             [tokens, head_num, head_dim], rows y_stride elements apart; it
  *                 overlaps nothing that the call reads
  *   softmax_max, softmax_sum: float32 [tokens, head_num, 8], all lanes written; or

@@ -126,11 +126,12 @@ struct ExtendParams {
   int sign;              // of the scale; the query rows are multiplied by it
   int least_span;        // shortest span of a CTA
   float scale_log2;      // |scale| log2(e), above 0 (1 where the scale is 0)
-  float bias;            // weights are multiplied by 2^bias
+  float bias;            // log2 of a factor that the sums of weights hold
   long long wait_ns;     // bound on every in-kernel wait
 };
 
 constexpr int kExtendRecord = 64;   // bytes of a CTA's record
+constexpr int kExtendBiasFp16 = 7, kExtendBiasBf16 = -8;   // (see paged_extend_tc.cuh)
 
 // How an extend call is run, and its workspace.
 struct ExtendPlan {

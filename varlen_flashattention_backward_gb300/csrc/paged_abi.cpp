@@ -334,7 +334,7 @@ fa_status fa_paged_extend_ex(const fa_paged_extend_args *args,
   p.scale_log2 = float(std::fabs(scale_log2));
   p.sign = p.scale_log2 == 0.f ? 0 : a.scale < 0 ? -1 : 1;
   if (p.sign == 0) p.scale_log2 = 1.f;
-  p.bias = dtype == FA_DTYPE_FP16 ? 7.f : 0.f;
+  p.bias = float(dtype == FA_DTYPE_FP16 ? kExtendBiasFp16 : dtype == FA_DTYPE_BF16 ? kExtendBiasBf16 : 0);
   p.wait_ns = options && options->wait_timeout_ns > 0 ? options->wait_timeout_ns : kDefaultWaitNs;
   p.least_span = 2;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);

@@ -366,7 +366,7 @@ struct Walk {
 // that comes out finite met no such value.  For one that does not, a warp looks
 // at the masked places that its block's tiles held, and where one of them is not finite
 // computes the row again from the keys that it sees.  (Without one, the row sees a value
-// that is not finite itself, and stays.)
+// that is not finite itself, or large ones whose sum passes fp32's range, and stays.)
 // ---------------------------------------------------------------------------
 template <typename T>
 __device__ __forceinline__ const T *cached(const ExtendParams &p, const void *cache, int b, int h, int key) {

@@ -21,7 +21,8 @@
 // are rounded to the type for the second product: half a step of the type relative
 // to each weight, of the size of y's own rounding; their sum is taken before.  fp16
 // weights carry 2^7, so that 2^8 of them still fits and 2^-31 of a row's largest
-// is still held.
+// is still held.  bf16 weights carry 2^-8 and so never pass 1: sums of products leave
+// fp32's range only where those of exp(S - max) would.
 //
 // Every wait is bounded; one that gives up sets FA_PAGED_TIMEOUT, and the CTA winds down
 // without waits but for its own copies and MMAs in flight.
@@ -433,6 +434,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using M = Dim<D>;
   constexpr int BN = M::BN;
   constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr float kBias = kBF16 ? kExtendBiasBf16 : kExtendBiasFp16;      // log2 of what weights carry
+  static_assert(!kBF16 || kBias == -kLazy, "bf16 weights stop at 1");
   extern __shared__ __align__(1024) uint8_t sm[];     // (a swizzle atom)
   Control *c = reinterpret_cast<Control *>(sm + 2 * M::kQ + M::kStages * M::kStage);
   const uint32_t sq = smem_u32(sm), ring = sq + 2 * M::kQ;
@@ -836,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = spent = wait(ctl, bar(c->spent[w]), (tiles - 1) & 1))) break;
             tc_fence_after();
           }
-          const float shift = (kBF16 ? 0.f : p.bias) - (m == -CUDART_INF_F ? 0.f : m);
+          const float shift = kBias - (m == -CUDART_INF_F ? 0.f : m);
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < kHalf; ++j) {
@@ -989,7 +992,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (mine) {
         if (whole) {
-          const float shift = (m == -CUDART_INF_F ? 0.f : m - top) - (kBF16 ? 0.f : p.bias);
+          const float shift = (m == -CUDART_INF_F ? 0.f : m - top) - kBias;
           write_stats(p, int64_t(it.r.start + t) * p.n + n, top * kLn2, l * ex2(shift));
         } else {
           part[D * kBR] = m;
