@@ -1,11 +1,13 @@
-"""Chunk attention at the ends of its types' ranges."""
+"""Chunk attention at the ends of its ranges: values at the top of the type's, and
+windows at the far end of the longest request."""
 
 import numpy as np
 import pytest
 import torch
 
-from _paged import f64
-from test_extend_gpu import Case
+from _paged import DTYPE, f64
+from test_extend_gpu import BIG, DEV, DTYPES, Case, dev
+from varlen_flashattention_backward_gb300 import binding as fa
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +39,25 @@ def test_small_values(dtype, new, past):
     c = Case(new, past, 4, 2, 64, dtype, page=16)
     c.cache[1][:] = c.cache[1].double() * 2.0 ** -118
     c.check()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_windows_at_the_end_of_the_longest_request(dtype):
+    # 2^30 keys: one page, named over and over.  A row at the last of them sees key 0 where
+    # the window ends 2^30 - 1 keys before it, and none where it ends before that.
+    page, pages = 65536, 16384
+    g = torch.Generator(device=DEV).manual_seed(1)
+    k = torch.randn(1, page, 1, 32, generator=g, device=DEV).to(DTYPE[dtype])
+    v = torch.randn(1, page, 1, 32, generator=g, device=DEV).to(DTYPE[dtype])
+    q = torch.randn(1, 2, 32, generator=g, device=DEV).to(DTYPE[dtype])
+    table = torch.zeros(1, pages, dtype=torch.int32, device=DEV)
+    lens, cu = dev(np.array([2 ** 30], np.int32)), dev(np.array([0, 1], np.int64))
+    for pre in (BIG, 2 ** 30, 2 ** 40):
+        y, top, total = fa.paged_extend(q, k, v, table, lens, cu, 0.2, pre, 1 - 2 ** 30, stats=True)
+        assert torch.equal(y[0, 0], v[0, 0, 0]) and torch.equal(y[0, 1], v[0, 0, 0])
+        # exp2 of the rounding of one score, 2^-24 of it, and its own error of 2^-22.
+        score = 0.2 * float((q.double().abs() * k[0, 0].double().abs()).sum(-1).max())
+        assert float((total - 1).abs().max()) <= score * 2.0 ** -24 + 2.0 ** -22
+        for after in (-2 ** 30, -2 ** 31, -2 ** 40):
+            y, top, total = fa.paged_extend(q, k, v, table, lens, cu, 0.2, pre, after, stats=True)
+            assert (y == 0).all() and (top == -float("inf")).all() and (total == 0).all()

@@ -121,7 +121,7 @@ struct ExtendParams {
   uint32_t *flags;
   int num_pages, page_size, page_shift;   // page_shift: log2(page_size), or -1
   int max_pages, batch, tokens, n, n_kv, d, group;
-  int pre, next;         // clamped to +-(2^30 - 1)
+  int pre, next;         // clamped to [-2^30, 2^30 - 1]
   int q_chunks, y_chunks, stat_chunks;   // rows of q, y, the statistics start on 16-byte boundaries
   int sign;              // of the scale; the query rows are multiplied by it
   int least_span;        // shortest span of a CTA

@@ -292,8 +292,9 @@ fa_status fa_paged_extend_ex(const fa_paged_extend_args *args,
   const auto chunks = [](const void *ptr, int64_t stride, int64_t in_16_bytes) {
     return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && stride % in_16_bytes == 0;
   };
-  // No position is further than 2^28 in front of the keys or 2^30 behind.
-  const auto window = [](int64_t x) { return int(x < 1 - kMaxKeys ? 1 - kMaxKeys : x > kMaxKeys - 1 ? kMaxKeys - 1 : x); };
+  // Positions are -2^28 + 1 to 2^30 - 1, keys 0 to 2^30 - 1: a window's bound of 2^30 - 1
+  // behind a row leaves none out, one of -2^30 none in.
+  const auto window = [](int64_t x) { return int(x < -kMaxKeys ? -kMaxKeys : x > kMaxKeys - 1 ? kMaxKeys - 1 : x); };
   char *work = static_cast<char *>(a.workspace);
   ExtendParams p{};
   p.q = a.q;

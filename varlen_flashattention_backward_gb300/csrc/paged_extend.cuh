@@ -53,7 +53,7 @@ __device__ __forceinline__ Request request_of(const ExtendParams &p, int b, int 
 }
 
 // Keys [lo, hi) that token t of the request sees.  (|pos| < 2^30 and the window's
-// bounds are clamped to +-(2^30 - 1): 32 bits do.)
+// bounds are clamped to [-2^30, 2^30 - 1]: 32 bits do.)
 __device__ __forceinline__ void keys_of(const ExtendParams &p, const Request &r, int t, int &lo, int &hi) {
   const int pos = r.len - r.n + t;
   lo = min(max(pos - p.pre, 0), r.len);
