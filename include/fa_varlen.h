@@ -656,8 +656,12 @@ fa_status fa_paged_decode_ex(const fa_paged_decode_args *args,
  * the statistics, so that a captured call can be replayed with fewer rows.
  * A row with no key to see, or whose every score is -inf, gets y = 0, max = -inf,
  * sum = 0.  What a row does not see, keys of its window's other rows and what the cache
- * holds behind a request's length, infinities and NaN too, has no influence.  The result
- * does not change from run to run on one device (fixed add order).
+ * holds behind a request's length, infinities and NaN too, has no influence.  (Next
+ * to a value of the request that it does not see and that is not finite, a row of y may be
+ * computed once more, with weights that are not rounded to the type; it then differs
+ * from what finite values there give by the size of that rounding.  Its statistics do
+ * not differ.)  The result does not change from run to run on one device (fixed add
+ * order).
  * Limits: tokens >= 0 and tokens * head_num <= 2^28 (FA_ERR_INVALID otherwise);
  * tokens == 0 returns FA_OK without a launch.  workspace: 16-byte aligned, at least
  * what fa_paged_extend_workspace_size gives on the current device; it serves one call

@@ -365,7 +365,8 @@ struct Walk {
 // which gives NaN where those are not finite.  Nothing is checked on the way there: a row
 // that comes out finite met no such value.  For one that does not, a warp looks
 // at the masked places that its block's tiles held, and where one of them is not finite
-// computes the row again from the keys that it sees.  (Without one, the row sees a value
+// computes the row again from the keys that it sees; its statistics, of which masked
+// scores are no part, stand.  (Without one, the row sees a value
 // that is not finite itself, or large ones whose sum passes fp32's range, and stays.)
 // ---------------------------------------------------------------------------
 template <typename T>
@@ -451,7 +452,6 @@ __device__ __noinline__ void mend_row(const ExtendParams &p, int b, int h, int i
   const float inv = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll
   for (int e = 0; e < PL; ++e) y[lane + 32 * e] = from_f<T>(o[e] * inv);
-  if (lane == 0) write_stats(p, int64_t(r.start + t) * p.n + n, top * kLn2, total);
 }
 
 // ---------------------------------------------------------------------------
