@@ -446,7 +446,7 @@ __device__ __noinline__ void mend_row(const ExtendParams &p, int b, int h, int i
       o[e] = o[e] * f + w * to_f<T>(vr[lane + 32 * e]);
       lost &= isnan(o[e]);
     }
-    if (isnan(total) && __all_sync(kFull, lost)) break;    // whatever follows
+    if (__all_sync(kFull, lost)) break;    // whatever follows
   }
   T *y = static_cast<T *>(p.y) + (r.start + t) * p.y_stride + int64_t(n) * D;
   const float inv = total == 0.f ? 0.f : 1.f / total;
@@ -551,30 +551,43 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) extend_join(const __grid_c
     }
   }
   if (!rec.flagged) return;
-  // The flags of the blocks that were not cut.
+  // The flags of the blocks that were not cut.  Every warp of the span looks at all of
+  // them and takes its turn of the rows: where a cache is full of such values, all rows are
+  // flagged (8192 tokens of 8 heads behind 20000, D 64, one column of NaN: 12.5 s with one
+  // warp at work, 0.5 s so; every column: 1.5 ms).
   const int words = rec.items * (BR / 32), words0 = rec.item0 * (BR / 32);
-  for (int w0 = (blockIdx.y * kJoinWarps + warp) * 32; w0 < words; w0 += gridDim.y * kJoinWarps * 32) {
+  const int turn = blockIdx.y * kJoinWarps + warp, turns = gridDim.y * kJoinWarps;
+  int at_turn = 0;       // of the next flagged row
+  for (int w0 = 0; w0 < words; w0 += 32) {
     const uint32_t mine = w0 + lane < words ? p.flags[int64_t(words0) + w0 + lane] : 0u;
     uint32_t some = __ballot_sync(kFull, mine != 0);
     while (some) {
       const int at = __ffs(some) - 1;
       some &= some - 1;
       uint32_t bits = __shfl_sync(kFull, mine, at);
-      int item = (words0 + w0 + at) / (BR / 32);
+      int item = (words0 + w0 + at) / (BR / 32), b = -1, n = 0;
       const int group = (words0 + w0 + at) % (BR / 32);
-      // Its request, then its head.
-      int b = 0, n = 0;
-      for (; b < p.batch; ++b) {
-        const Request r = request_of(p, b, err);
-        n = blocks_of<BR>(p, r);
-        if (item < n * p.n_kv) break;
-        item -= n * p.n_kv;
-      }
-      if (b >= p.batch) continue;
-      while (bits) {
-        const int bit = __ffs(bits) - 1;
-        bits &= bits - 1;
-        mend_row<T, D, BR, BN>(p, b, item / n, item % n, group * 32 + bit);
+      for (; bits; bits &= bits - 1) {
+        const bool own = at_turn == turn;
+        if (++at_turn == turns) at_turn = 0;
+        if (!own) continue;
+        // Its request (32 at a time), then its head.
+        for (int b0 = 0; b < 0 && b0 < p.batch; b0 += 32) {
+          const int blocks = b0 + lane < p.batch ? blocks_of<BR>(p, request_of(p, b0 + lane, err)) : 0;
+          int upto = blocks * p.n_kv;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(kFull, upto, o);
+            if (lane >= o) upto += u;
+          }
+          const uint32_t beyond = __ballot_sync(kFull, upto > item);
+          const int k = beyond ? __ffs(beyond) - 1 : 31;
+          n = __shfl_sync(kFull, blocks, k);
+          item -= __shfl_sync(kFull, upto, k) - (beyond ? n * p.n_kv : 0);
+          if (beyond) b = b0 + k;
+        }
+        if (b < 0) break;
+        mend_row<T, D, BR, BN>(p, b, item / n, item % n, group * 32 + __ffs(bits) - 1);
       }
     }
   }
