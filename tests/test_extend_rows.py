@@ -42,3 +42,14 @@ def test_the_last_of_2048_requests_descends(dtype):
     c.check(error=fa.FA_PAGED_ROWS)
     c.cu[2047:] = 2046, 2048
     c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_every_request_descends(dtype):
+    from test_extend_gpu import Case
+    c = Case([1] * 2048, [3] * 2048, 64, 1, 32, dtype, page=4)
+    c.cu = np.arange(2048, -1, -1, dtype=np.int64)
+    c.check(error=fa.FA_PAGED_ROWS)
+    c.cu[::2], c.cu[1::2] = 2048, 0
+    c.check(error=fa.FA_PAGED_ROWS)

@@ -32,6 +32,9 @@ constexpr uint32_t kFull = 0xffffffffu;
 // ---------------------------------------------------------------------------
 // (kSwitch 2: prompts 817 -> 796 us, a step of single tokens and chunks 236 -> 256.)
 constexpr int kSwitch = 1;
+// Units of a request that rules the call out: more than 2^28 / 64 blocks of 2^30 / 32 tiles
+// have, and 2048 times as many still fit.
+constexpr int64_t kTooMany = int64_t(1) << 49;
 
 struct Request {
   int start, n;   // rows of q
@@ -64,7 +67,6 @@ __device__ __forceinline__ void keys_of(const ExtendParams &p, const Request &r,
 struct Block {
   int row0, rows;      // its packed rows
   int tile0, tiles;    // the keys' tiles that any of them may see
-  int lo, hi;          // the keys that any of them sees
 };
 
 template <int BR, int BN>
@@ -72,14 +74,11 @@ __device__ __forceinline__ Block block_of(const ExtendParams &p, const Request &
   Block k;
   k.row0 = i * BR;
   k.rows = min(BR, r.n * p.group - k.row0);
-  int hi, unused;
-  keys_of(p, r, k.row0 / p.group, k.lo, unused);
+  int lo, hi, unused;
+  keys_of(p, r, k.row0 / p.group, lo, unused);
   keys_of(p, r, (k.row0 + k.rows - 1) / p.group, unused, hi);
-  k.tile0 = k.lo / BN;
-  k.tiles = hi > k.lo ? (hi + BN - 1) / BN - k.tile0 : 0;
-  // Windows of neighbouring rows lie one key apart, so that together they leave no gap;
-  // where they are empty, what lies between two of them is nobody's.
-  k.hi = p.pre + p.next < 0 ? k.lo : hi;
+  k.tile0 = lo / BN;
+  k.tiles = hi > lo ? (hi + BN - 1) / BN - k.tile0 : 0;
   return k;
 }
 
@@ -120,19 +119,19 @@ __device__ bool measure(const ExtendParams &p, Measure &m, Line &line, Place &at
   constexpr int kLanes = 8;      // that share a request's blocks
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int err = 0;
-  bool descends = false;
 #pragma unroll 1
   for (int b0 = 0; b0 < p.batch; b0 += THREADS / kLanes) {
     const int b = b0 + tid / kLanes;
     int64_t units = 0;
     int n = 0;
     if (b < p.batch) {
+      const bool descends = p.cu[b + 1] < p.cu[b];
       const Request r = request_of(p, b, err);
-      descends |= p.cu[b + 1] < p.cu[b];
       if (tid % kLanes == 0) m.request[b] = r;
       n = blocks_of<BR>(p, r);
 #pragma unroll 1
       for (int i = tid % kLanes; i < n; i += kLanes) units += block_of<BR, BN>(p, r, i).tiles + kSwitch;
+      if (descends) units = tid % kLanes == 0 ? kTooMany : 0;
     }
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) units += __shfl_xor_sync(kFull, units, o);
@@ -142,15 +141,11 @@ __device__ bool measure(const ExtendParams &p, Measure &m, Line &line, Place &at
     }
   }
   if (err && blockIdx.x == 0 && p.error) atomicOr(p.error, err);
-  // Requests whose bounds descend could share rows: nothing is done then.  (Ascending ones
-  // have rows of their own, so that no more blocks come together than the workspace has
-  // flags for.)
-  line = Line{};
-  if (__syncthreads_or(descends)) return false;
-  // Prefix sums: each thread a run of requests, each warp, all warps.
+  __syncthreads();
+  // Prefix sums: each thread a run of requests, each warp, all warps.  (Blocks of requests
+  // whose bounds descend need not fit 32 bits; they are not used.)
   const int per = (p.batch + THREADS - 1) / THREADS;
-  int64_t own = 0;
-  int own_blocks = 0;
+  int64_t own = 0, own_blocks = 0;
 #pragma unroll 1
   for (int k = 0; k < per; ++k) {
     const int b = tid * per + k;
@@ -159,12 +154,10 @@ __device__ bool measure(const ExtendParams &p, Measure &m, Line &line, Place &at
       own_blocks += m.blocks[b + 1];
     }
   }
-  int64_t x = own;
-  int y = own_blocks;
+  int64_t x = own, y = own_blocks;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(kFull, x, o);
-    const int v = __shfl_up_sync(kFull, y, o);
+    const int64_t u = __shfl_up_sync(kFull, x, o), v = __shfl_up_sync(kFull, y, o);
     if (lane >= o) {
       x += u;
       y += v;
@@ -173,11 +166,10 @@ __device__ bool measure(const ExtendParams &p, Measure &m, Line &line, Place &at
   __syncthreads();
   if (lane == 31) {
     m.sum64[warp] = x;
-    m.sum32[warp] = y;
+    m.sum32[warp] = int(min(y, int64_t(1) << 30));
   }
   __syncthreads();
-  int64_t before = x - own, all = 0;
-  int before_blocks = y - own_blocks;
+  int64_t before = x - own, before_blocks = y - own_blocks, all = 0;
 #pragma unroll 1
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) {
@@ -193,7 +185,7 @@ __device__ bool measure(const ExtendParams &p, Measure &m, Line &line, Place &at
       before += m.upto[b + 1];
       before_blocks += m.blocks[b + 1];
       m.upto[b + 1] = before;
-      m.blocks[b + 1] = before_blocks;
+      m.blocks[b + 1] = int(min(before_blocks, int64_t(1) << 30));
     }
   }
   if (tid == 0) {
@@ -201,7 +193,10 @@ __device__ bool measure(const ExtendParams &p, Measure &m, Line &line, Place &at
     m.blocks[0] = 0;
   }
   __syncthreads();
-  line.units = all * p.n_kv;
+  // Requests whose bounds descend could share rows: nothing is done then.  (Ascending ones
+  // have rows of their own, so that no more blocks come together than the workspace has
+  // flags for.)
+  line.units = all >= kTooMany ? 0 : all * p.n_kv;
   line.span = max((line.units + gridDim.x - 1) / gridDim.x, int64_t(p.least_span));
   at.at = line.span * blockIdx.x;
   at.left = min(line.span, line.units - at.at);
@@ -266,7 +261,8 @@ struct Record {
   Request r;
   int32_t flagged;         // some row of the blocks that it finished is to be looked at
   int32_t item0, items;    // those blocks, and others beside them
-  int32_t pad[3];
+  int32_t odd;             // a tile had a key with a bad page
+  int32_t pad[2];
 };
 static_assert(sizeof(Record) == kExtendRecord, "records");
 
@@ -454,10 +450,52 @@ __device__ __noinline__ void mend_row(const ExtendParams &p, int b, int h, int i
   for (int e = 0; e < PL; ++e) y[lane + 32 * e] = from_f<T>(o[e] * inv);
 }
 
+// The request of an item and how many blocks a key head of it has; `item` is counted from
+// the request's first then.  By a whole warp, 32 requests at a time; b = -1 where there
+// is none (flags that a call whose wait ran out has not written).
+template <int BR>
+__device__ __noinline__ int2 find_request(const ExtendParams &p, int &item) {
+  const int lane = threadIdx.x & 31;
+  int err = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    const int blocks = b0 + lane < p.batch ? blocks_of<BR>(p, request_of(p, b0 + lane, err)) : 0;
+    int upto = blocks * p.n_kv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(kFull, upto, o);
+      if (lane >= o) upto += u;
+    }
+    const uint32_t beyond = __ballot_sync(kFull, upto > item);
+    const int k = beyond ? __ffs(beyond) - 1 : 31, n = __shfl_sync(kFull, blocks, k);
+    item -= __shfl_sync(kFull, upto, k) - (beyond ? n * p.n_kv : 0);
+    if (beyond) return make_int2(b0 + k, n);
+  }
+  return make_int2(-1, 0);
+}
+
+// Reports the bad pages of request b that any of its rows sees; by a warp, where a tile had
+// some (looked for key by key in the loaders, 2 to 10% of calls whose keys come in pieces):
+// tiles begin in front of a window and end behind it.  (Windows of neighbouring rows
+// lie one key apart, so that together they leave no gap; where they are empty, what lies
+// between two of them is nobody's.)
+__device__ __noinline__ void report_pages(const ExtendParams &p, int b) {
+  int lo, hi, unused, err = 0;
+  const Request r = request_of(p, b, err);
+  keys_of(p, r, 0, lo, unused);
+  keys_of(p, r, r.n - 1, unused, hi);
+  if (r.n == 0 || p.pre + p.next < 0 || lo >= hi) return;
+  bool bad = false;
+  for (int i = lo / p.page_size + (threadIdx.x & 31); i <= (hi - 1) / p.page_size; i += 32) {
+    const int page = p.table[b * p.table_stride + i];
+    bad |= page < 0 || page >= p.num_pages;
+  }
+  if (bad && p.error) atomicOr(p.error, FA_PAGED_BAD_PAGE);
+}
+
 // ---------------------------------------------------------------------------
-// Adds the parts of the blocks that were cut, and mends rows.  CTA (x, y) takes 32
-// rows of the block that begins last in span x; a warp takes D / 8 columns, a lane a
-// row.  Bound by latency, of the record, then of the parts, which lie in the L2: two are
+// Adds the parts of the blocks that were cut, mends rows and reports bad pages.  CTA
+// (x, y) takes 32 rows of the block that begins last in span x; a warp takes D / 8
+// columns, a lane a row.  Bound by latency, of the record, then of the parts, which lie in the L2: two are
 // on the way at a time (20 parts a block: 13 us of a call of 42; four on the way take as
 // long there, and 10 us more in cross attention).
 // ---------------------------------------------------------------------------
@@ -475,7 +513,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) extend_join(const __grid_c
   const Record *records = reinterpret_cast<const Record *>(p.records);
   const Record rec = records[blockIdx.x];
   const int row0 = blockIdx.y * 32, row = row0 + lane;
-  int err = 0;
   if (rec.cut) {
     const Request r = rec.r;
     const Block k = block_of<BR, BN>(p, r, rec.i);
@@ -550,13 +587,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) extend_join(const __grid_c
       }
     }
   }
+  if (!(rec.flagged | rec.odd)) return;
+  const int turn = blockIdx.y * kJoinWarps + warp, turns = gridDim.y * kJoinWarps;
+  if (rec.odd) {
+    int first = rec.item0, last = rec.item0 + rec.items - 1;
+    const int b0 = find_request<BR>(p, first).x, b1 = find_request<BR>(p, last).x;
+    for (int b = max(b0, 0) + turn; b <= b1; b += turns) report_pages(p, b);
+  }
   if (!rec.flagged) return;
   // The flags of the blocks that were not cut.  Every warp of the span looks at all of
   // them and takes its turn of the rows: where a cache is full of such values, all rows are
   // flagged (8192 tokens of 8 heads behind 20000, D 64, one column of NaN: 12.5 s with one
   // warp at work, 0.5 s so; every column: 1.5 ms).
   const int words = rec.items * (BR / 32), words0 = rec.item0 * (BR / 32);
-  const int turn = blockIdx.y * kJoinWarps + warp, turns = gridDim.y * kJoinWarps;
   int at_turn = 0;       // of the next flagged row
   for (int w0 = 0; w0 < words; w0 += 32) {
     const uint32_t mine = w0 + lane < words ? p.flags[int64_t(words0) + w0 + lane] : 0u;
@@ -565,29 +608,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) extend_join(const __grid_c
       const int at = __ffs(some) - 1;
       some &= some - 1;
       uint32_t bits = __shfl_sync(kFull, mine, at);
-      int item = (words0 + w0 + at) / (BR / 32), b = -1, n = 0;
+      int item = (words0 + w0 + at) / (BR / 32);
+      int2 found = make_int2(-1, 0);
       const int group = (words0 + w0 + at) % (BR / 32);
       for (; bits; bits &= bits - 1) {
         const bool own = at_turn == turn;
         if (++at_turn == turns) at_turn = 0;
         if (!own) continue;
-        // Its request (32 at a time), then its head.
-        for (int b0 = 0; b < 0 && b0 < p.batch; b0 += 32) {
-          const int blocks = b0 + lane < p.batch ? blocks_of<BR>(p, request_of(p, b0 + lane, err)) : 0;
-          int upto = blocks * p.n_kv;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(kFull, upto, o);
-            if (lane >= o) upto += u;
-          }
-          const uint32_t beyond = __ballot_sync(kFull, upto > item);
-          const int k = beyond ? __ffs(beyond) - 1 : 31;
-          n = __shfl_sync(kFull, blocks, k);
-          item -= __shfl_sync(kFull, upto, k) - (beyond ? n * p.n_kv : 0);
-          if (beyond) b = b0 + k;
-        }
-        if (b < 0) break;
-        mend_row<T, D, BR, BN>(p, b, item / n, item % n, group * 32 + __ffs(bits) - 1);
+        if (found.x < 0) found = find_request<BR>(p, item);
+        if (found.x < 0) break;
+        mend_row<T, D, BR, BN>(p, found.x, item / found.y, item % found.y, group * 32 + __ffs(bits) - 1);
       }
     }
   }

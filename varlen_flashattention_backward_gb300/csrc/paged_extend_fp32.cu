@@ -58,13 +58,12 @@ __global__ void __launch_bounds__(kThreads, D <= 64 ? 3 : 2) extend_fp32_kernel(
   }
   asm volatile("griddepcontrol.launch_dependents;");
   __syncthreads();
-  int err = 0;
   Segment seg;
   // (Every thread walks for itself; the barriers below do not depend on what it reads
   // but for the number of segments and tiles, which one thread tells.)
   __shared__ Segment s_seg;
-  __shared__ int s_more, s_flagged;
-  if (tid == 0) s_flagged = 0;
+  __shared__ int s_more, s_flagged, s_odd;
+  if (tid == 0) s_flagged = s_odd = 0;
   while (true) {
     if (tid == 0) {
       s_more = walk.next(p, seg);
@@ -110,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, D <= 64 ? 3 : 2) extend_fp32_kernel(
       const float *src = j < r.len ? cached<float>(p, cache, seg.b, seg.h, j) : nullptr;
       if (fine != nullptr && part == 0) {
         fine[key] = src != nullptr;
-        if (j >= seg.k.lo && j < seg.k.hi && src == nullptr) err |= FA_PAGED_BAD_PAGE;
+        if (j < r.len && src == nullptr) s_odd = 1;
       }
       const float *from = src != nullptr ? src : static_cast<const float *>(cache);
 #pragma unroll
@@ -271,9 +270,9 @@ __global__ void __launch_bounds__(kThreads, D <= 64 ? 3 : 2) extend_fp32_kernel(
   __syncthreads();
   if (tid == 0) {
     walk.rec.flagged = s_flagged;
+    walk.rec.odd = s_odd;
     reinterpret_cast<Record *>(p.records)[blockIdx.x] = walk.rec;
   }
-  if (err && p.error) atomicOr(p.error, err);
 }
 
 template <int D>

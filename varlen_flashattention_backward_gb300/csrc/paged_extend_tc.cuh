@@ -105,7 +105,6 @@ __device__ __forceinline__ Stage place_of(int kv, int tile) {
 struct Item {
   Request r;
   int row0, rows;      // packed rows
-  int lo, hi;          // the keys that any of them sees
   int b, h, key0, steps;  // first key of its first tile; turns of a softmax warpgroup, both together
   int both;            // the halves have rows of their own
   int tile;            // number of its first tile in the CTA
@@ -120,7 +119,7 @@ struct Control {
   // ready: scores; taken: they have been read; weights: of a half of the keys; half, spent:
   // the products of those halves with the values are done.
   uint32_t tmem;
-  int abort, flagged;
+  int abort, flagged, odd;
   Item item[kItems];
   alignas(16) uint32_t mask[kMasks][4];   // which keys' pages are the cache's
   float part[3][128];                     // the second half's sums of a shared block
@@ -267,9 +266,8 @@ struct Loader {
   uint32_t ring;
   Ctl ctl;
   int lane, kv;                        // kv: 0 for K, 1 for V
-  int err = 0;
+  bool odd = false;                    // some key has a bad page
   int tiles = 0;                       // so far
-  int lo = 0, hi = 0;                  // the keys of the segment that any row sees
 
   __device__ __forceinline__ uint32_t bar(uint64_t &b) const { return smem_u32(&b); }
 
@@ -330,6 +328,7 @@ struct Loader {
     const T *cache = static_cast<const T *>(kv ? p.vc : p.kc);
     const int ch = lane & (kAcross - 1), sub = lane / kAcross;
     const uint32_t dst = ring + place.stage * M::kStage + (ch >> 3) * M::kPanel;
+    int good = 0;
 #pragma unroll 1
     for (int k = 0; k < kRows; ++k) {
       const int key = key0 + k * 32 + lane;
@@ -340,14 +339,11 @@ struct Loader {
                                           : k == 1 ? pages.of[1]
                                           : k == 2 ? pages.of[kRows - 2]
                                                    : pages.of[kRows - 1];
-      int64_t at = -1;     // of the key's row in the cache
-      if (key < len) {
-        if (page >= 0 && page < p.num_pages)
-          at = page * p.page_stride + token_of(key) * p.token_stride + h * p.head_stride;
-        else if (key >= lo && key < hi)
-          err |= FA_PAGED_BAD_PAGE;
-      }
+      int64_t at = -1;     // of the key's row in the cache (keys behind the request's have page -1)
+      if (page >= 0 && page < p.num_pages)
+        at = page * p.page_stride + token_of(key) * p.token_stride + h * p.head_stride;
       const uint32_t word = __ballot_sync(kFull, at >= 0);
+      good += __popc(word);
       if (kv == 0 && lane == 0) c->mask[which][k] = word;
 #pragma unroll 4
       for (int r0 = 0; r0 < 32; r0 += 32 / kAcross) {
@@ -358,6 +354,7 @@ struct Loader {
                      cache + (from >= 0 ? from + ch * 8 : 0), from >= 0);
       }
     }
+    odd |= good < min(len - key0, M::BN);
     if (box) {      // the MMA warp does not expect pieces here
       cp_async_wait_all();
       fence_proxy_async_smem();
@@ -384,13 +381,13 @@ struct Loader {
   // No copy may still be writing shared memory when the CTA exits, nor the arrival that
   // counts pieces in, which comes behind them.
   __device__ __forceinline__ void drain(long long ns) {
+    if (odd && lane == 0) c->odd = 1;
     cp_async_wait_all();
     const int never = 0, stages = kv ? M::kStagesV : M::kStagesK;
     for (int t = tiles > stages ? tiles - stages : 0; t < tiles; ++t) {
       const Stage at = place_of<D>(kv, t);
       mbar_wait(bar(c->full[at.stage]), uint32_t(at.turn) & 1, ns, &never);
     }
-    if (err && p.error) atomicOr(p.error, err);
   }
 };
 
@@ -446,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long drain_ns = p.wait_ns > 1000000000LL ? p.wait_ns : 1000000000LL;
 
   if (tid == 0) {
-    c->abort = c->flagged = 0;
+    c->abort = c->flagged = c->odd = 0;
     for (int i = 0; i < M::kStages; ++i) {
       mbar_init(bar(c->full[i]), 1);
       mbar_init(bar(c->empty[i]), 1);
@@ -505,8 +502,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               it.r = seg.r;
               it.row0 = seg.k.row0;
               it.rows = seg.k.rows;
-              it.lo = seg.k.lo;
-              it.hi = seg.k.hi;
               it.b = seg.b;
               it.h = seg.h;
               it.key0 = (seg.k.tile0 + seg.t0) * BN;
@@ -524,8 +519,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const int len = it.r.len, b = it.b, h = it.h, key0 = it.key0, end = it.end, count = it.steps >> it.both;
-        load.lo = it.lo;
-        load.hi = it.hi;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(c->item_empty[slot]));
         if (end || !load.all(len, b, h, key0, count)) break;
@@ -1012,6 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) {
     c->record.flagged = c->flagged;
+    c->record.odd = c->odd;
     reinterpret_cast<Record *>(p.records)[blockIdx.x] = c->record;
   }
 }
