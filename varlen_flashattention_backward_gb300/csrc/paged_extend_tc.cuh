@@ -27,14 +27,15 @@
 // Every wait is bounded; one that gives up sets FA_PAGED_TIMEOUT, and the CTA winds down
 // without waits but for its own copies and MMAs in flight.
 //
-// 2048 tokens behind 30000, 32 heads on 8, D 128, bf16: 626 us, 1660 TFLOP/s, 88% of the
-// measured peak.  A turn of both halves takes 2900 cycles, their products 2048; what is
+// 2048 tokens behind 30000, 32 heads on 8, D 128, bf16: 635 us, 1640 TFLOP/s, for the first
+// 60 ms at full clocks (87% of the measured burst peak), and 702 us, 1480 TFLOP/s, from
+// then on, under the power cap (87% of the sustained one).  A turn of both halves takes 2900 cycles, their products 2048; what is
 // left is the way of a half from scores over softmax and products to its next scores,
 // which two halves cannot hide altogether.  Instruction fetches were the largest stall
 // of all: with the two halves of a tile unrolled the loop took 710 us, hence one copy of
 // the code per purpose, and rare paths out of line.  64 drafts of 5 tokens over 1024 to
-// 8192 keys: 217 us, 6.0 TB/s, 89% of the copy bandwidth.  At D 64 and 32 the softmax
-// bounds it (the first case 542 us at D 64, 2600 cycles a turn, 1024 of them
+// 8192 keys: 218 us, 6.0 TB/s, 88% of the copy bandwidth.  At D 64 and 32 the softmax
+// bounds it (the first case 527 us at D 64, 2600 cycles a turn, 1024 of them
 // exponentials).
 
 #include <cuda.h>
