@@ -382,7 +382,6 @@ struct Loader {
   // No copy may still be writing shared memory when the CTA exits, nor the arrival that
   // counts pieces in, which comes behind them.
   __device__ __forceinline__ void drain(long long ns) {
-    if (odd && lane == 0) c->odd = 1;
     cp_async_wait_all();
     const int never = 0, stages = kv ? M::kStagesV : M::kStagesK;
     for (int t = tiles > stages ? tiles - stages : 0; t < tiles; ++t) {
@@ -524,6 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(c->item_empty[slot]));
         if (end || !load.all(len, b, h, key0, count)) break;
       }
+      if (load.odd && lane == 0) c->odd = 1;
       load.drain(drain_ns);
       if (warp == 8 && lane == 0) c->record = walk.rec;
     } else if (warp == 11) {
