@@ -32,6 +32,22 @@ def test_large_values_behind_small_ones(dtype, dim, new, past, at):
     assert torch.isfinite(y).all() and f64(y).max() > 2.0 ** 115
 
 
+@pytest.mark.parametrize("dim", [32, 128, 192])
+@pytest.mark.parametrize("unseen", [None, float("nan"), float("inf")])
+def test_many_large_values_beside_one_that_is_not_finite(dim, unseen):
+    # 200 keys and more that weigh alike, each 2^121, sum up to 2^128 and more where weights are
+    # 1.  In bf16 they are 2^-8, in rows that are computed once more too.
+    c = Case([100, 70], [200, 300], 2, 1, dim, "bf16", page=16)
+    c.cache[0][:] = 0
+    c.cache[1][:] = 2.0 ** 121
+    if unseen is not None:
+        for b, key in ((0, 290), (1, 365)):
+            c.cache[1][c.table[b, key // 16], key % 16, 0, 3] = unseen
+    y = c.check()
+    if unseen is not None:
+        assert (f64(y[:90, :, 3]) == 2.0 ** 121).all() and not np.isfinite(f64(y[90:100, :, 3])).any()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("new,past", [([1, 5], [300, 90]), ([200], [300]), ([3], [9000])])
 def test_small_values(dtype, new, past):

@@ -433,7 +433,7 @@ __device__ __noinline__ void mend_row(const ExtendParams &p, int b, int h, int i
     for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(kFull, s, x);
     s *= p.scale_log2;
     const float m = fmaxf(top, s), ref = m == -CUDART_INF_F ? 0.f : m;
-    const float f = exp2f(top - ref), w = exp2f(s - ref);
+    const float f = exp2f(top - ref), w = exp2f(s - ref + p.bias);   // (as large as in the first place)
     top = m;
     total = total * f + w;
     bool lost = true;
