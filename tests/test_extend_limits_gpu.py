@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+from _extend import check_extend
 from _paged import DTYPE, f64
 from test_extend_gpu import BIG, DEV, DTYPES, Case, dev
 from varlen_flashattention_backward_gb300 import binding as fa
@@ -55,6 +56,28 @@ def test_small_values(dtype, new, past):
     c = Case(new, past, 4, 2, 64, dtype, page=16)
     c.cache[1][:] = c.cache[1].double() * 2.0 ** -118
     c.check()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [32, 64, 192])
+@pytest.mark.parametrize("new,past", [([1], [0]), ([5, 200], [3, 300]), ([3], [9000]), ([300], [0])])
+def test_scores_of_minus_infinity_beside_values_that_are_not_finite(dtype, dim, new, past):
+    # y = 0, whatever the values are; next to them a head whose keys are finite.
+    c = Case(new, past, 4, 2, dim, dtype, page=16)
+    c.q[:] = c.q.abs().clamp(min=0.1)
+    c.cache[0][:, :, 0] = -float("inf")
+    c.cache[1][:, ::2, 0] = float("inf")
+    c.cache[1][:, 1::3, 0] = float("nan")
+    y, top, total, error = c.run()
+    own = slice(0, int(c.cu[-1]))
+    assert error == 0 and (y[own, :2] == 0).all()
+    assert (top[own, :2] == -float("inf")).all() and (total[own, :2] == 0).all()
+    c.q[:, :2] = 0.0      # (out of the oracle's way)
+    c.cache[0][:, :, 0] = 0.0
+    c.cache[1][:, :, 0] = 0.0
+    ref = c.oracle()
+    check_extend({k: x if k in ("error", "owned", "keys") else x[:, 2:] for k, x in ref.items()}, dim, dtype,
+                 y[:, 2:], top[:, 2:], total[:, 2:])
 
 
 @pytest.mark.parametrize("dtype", DTYPES)

@@ -60,3 +60,25 @@ def test_rows_of_many_requests(dtype, batch, heads, heads_kv):
             last = int(c.lens[b]) - 1
             c.cache[1][c.table[b, last // 4], last % 4, b % heads_kv, 3] = float("nan")
     c.check()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_row_whose_first_scores_are_minus_infinity(dtype):
+    # It sees NaN with weight 0 first and finite values then, which makes NaN, beside values
+    # that it does not see; a row that sees no other scores stays 0.
+    c = Case([40, 3], [60, 90], 2, 1, 64, dtype, page=16)
+    c.q[:] = c.q.abs().clamp(min=0.1)
+    for b in range(2):
+        for j in range(int(c.lens[b])):
+            at = c.table[b, j // 16], j % 16, 0
+            if j < 50 or b == 1:
+                c.cache[0][at] = -float("inf")
+            if j < 50 or j >= int(c.lens[b]) - 1:
+                c.cache[1][at] = float("nan")
+    y, top, total, error = c.run()
+    assert error == 0 and y[:40].isnan().all() and (total[:40] > 0).all()
+    assert (y[40:43] == 0).all() and (total[40:43] == 0).all() and (top[40:43] == -float("inf")).all()
+    y, _, total, _ = c.run(after=-60)            # row i sees keys 0 to i
+    assert (y[:40] == 0).all() and (total[:40] == 0).all()
+    y, _, total, _ = c.run(after=-20)            # 0 to 40 + i
+    assert (y[:10] == 0).all() and (total[:10] == 0).all() and y[10:40].isnan().all()

@@ -362,8 +362,9 @@ struct Walk {
 // that comes out finite met no such value.  For one that does not, a warp looks
 // at the masked places that its block's tiles held, and where one of them is not finite
 // computes the row again from the keys that it sees; its statistics, of which masked
-// scores are no part, stand.  (Without one, the row sees a value
-// that is not finite itself, or large ones whose sum passes fp32's range, and stays.)
+// scores are no part, stand.  (Without one, the row sees a value that is not finite itself, or
+// large ones whose sum passes fp32's range, and stays; but it becomes 0 where all of its
+// scores are -inf.)
 // ---------------------------------------------------------------------------
 template <typename T>
 __device__ __forceinline__ const T *cached(const ExtendParams &p, const void *cache, int b, int h, int key) {
@@ -414,7 +415,7 @@ __device__ __noinline__ void mend_row(const ExtendParams &p, int b, int h, int i
 #pragma unroll
     for (int e = 0; e < PL; ++e) found |= !isfinite(to_f<T>(v[lane + 32 * e]));
   }
-  if (!__any_sync(kFull, found)) return;
+  found = __any_sync(kFull, found);
   const T *q = static_cast<const T *>(p.q) + (r.start + t) * p.q_stride + int64_t(n) * D;
   float qd[PL], o[PL];
 #pragma unroll
@@ -442,12 +443,14 @@ __device__ __noinline__ void mend_row(const ExtendParams &p, int b, int h, int i
       o[e] = o[e] * f + w * to_f<T>(vr[lane + 32 * e]);
       lost &= isnan(o[e]);
     }
+    if (total == 0.f) continue;
+    if (!found) return;
     if (__all_sync(kFull, lost)) break;    // whatever follows
   }
   T *y = static_cast<T *>(p.y) + (r.start + t) * p.y_stride + int64_t(n) * D;
   const float inv = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll
-  for (int e = 0; e < PL; ++e) y[lane + 32 * e] = from_f<T>(o[e] * inv);
+  for (int e = 0; e < PL; ++e) y[lane + 32 * e] = from_f<T>(total == 0.f ? 0.f : o[e] * inv);
 }
 
 // The request of an item and how many blocks a key head of it has; `item` is counted from
